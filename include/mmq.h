@@ -56,7 +56,7 @@ enum mmq_status {
     MMQ_ERR_OVERFLOW = -4,  /* a size beyond the kernels' index range (see limits below) */
     MMQ_ERR_DEVICE = -5,    /* no HIP device, or the current device is not gfx950 */
     MMQ_ERR_HIP = -6,       /* the HIP runtime reported an error at launch */
-    MMQ_ERR_KERNEL = -7     /* unknown kernel or format id, or a kernel outside its token range */
+    MMQ_ERR_KERNEL = -7     /* unknown kernel, format or activation id, or a kernel outside its token range */
 };
 
 /* Size limits (MMQ_ERR_OVERFLOW beyond them): n, m <= 2^31 - 1; k <= 2^24;
@@ -347,6 +347,176 @@ enum mmq_format {
  * k not a positive multiple of 256, MMQ_ERR_KERNEL for an unknown format.
  */
 int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n);
+
+/*
+ * mmq_fold_epilogue - a fold entry point with an epilogue: what follows the
+ * matmul elementwise is done as its results are stored, in float32, with one
+ * rounding at a binary16 store.
+ *
+ *   out[t][o] = act( fold[t][o] + bias[o] ) + residual[t][o]
+ *
+ * where fold is the float32 result of the entry point of `format` for the
+ * same arguments, bit for bit (with every operand absent and MMQ_ACT_NONE the
+ * call is that entry point).  Outputs and residuals may be rows of larger
+ * arrays (strides), and the residual may be the output itself (same type and
+ * stride: x += W h); otherwise they must not overlap.
+ *
+ *   w, q, ds : as for the entry point of `format` (q: its int8 codes or its
+ *              operand tiles); m, k, n and their limits too.
+ *   out      : float32 or binary16 [n][out_stride], columns 0 .. m - 1 written.
+ * Errors as for that entry point; MMQ_ERR_NULL for a NULL epilogue,
+ * MMQ_ERR_KERNEL for an unknown format or activation, MMQ_ERR_SHAPE for a
+ * stride below m, MMQ_ERR_ALIGN for a bias or residual not 16-byte aligned.
+ */
+enum mmq_activation {
+    MMQ_ACT_NONE = 0,
+    MMQ_ACT_RELU = 1,      /* max(v, 0) */
+    MMQ_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+    MMQ_ACT_GELU = 3,      /* v * Phi(v) = v * erfc(-v / sqrt(2)) / 2 */
+    MMQ_ACT_GELU_TANH = 4  /* v * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) / 2 */
+};
+
+typedef struct mmq_epilogue {
+    const float *bias;        /* [m], or NULL (mmq_fold_grouped: [experts][m]) */
+    const void *residual;     /* [n][residual_stride], or NULL */
+    int64_t residual_stride;  /* elements between rows; 0 = m */
+    int64_t out_stride;       /* elements between output rows; 0 = m */
+    int activation;           /* enum mmq_activation */
+    int residual_f16;         /* residual is binary16 (else float32) */
+    int out_f16;              /* out is binary16 (else float32) */
+} mmq_epilogue;
+
+int mmq_fold_epilogue(int format, const void *w, int64_t m, int64_t k, const void *q, const uint32_t *ds,
+                      int64_t n, const mmq_epilogue *epilogue, void *out, hipStream_t stream);
+
+/*
+ * mmq_fold_grouped - matrix products grouped by expert, with ragged sizes that
+ * only the device knows: slots s with offsets[e] <= s < offsets[e+1] belong
+ * to expert e and are multiplied by its matrix,
+ *
+ *   out[s][o] = act( fold(W[e], row r(s) of q)[o] + bias[e][o] ) + residual[s][o]
+ *
+ * with r(s) = rows[s], or s without rows.  Any expert may have no slots, and
+ * any row may be taken any number of times.  Slots outside
+ * [offsets[0], offsets[experts]) are left as they were.  The call reads
+ * nothing back and has no launch that depends on the offsets' values, so it
+ * can be captured into a graph and replayed over new ones.
+ *
+ *   format  : MMQ_FORMAT_Q4K or MMQ_FORMAT_Q6K (others: MMQ_ERR_KERNEL).
+ *   w       : [experts] matrices of [m][k], one behind the other; with more
+ *             than one expert the bytes of a matrix must be a multiple of 16
+ *             (MMQ_ERR_ALIGN; always so in q4_K, in q6_K where m*(k/256) is a
+ *             multiple of 8).
+ *   q, ds   : [tokens] rows, as for the fold entry points.
+ *   rows    : int32 [slots], 0 <= rows[s] < tokens, or NULL (then tokens must
+ *             be at least slots, MMQ_ERR_SHAPE).  Not read outside the groups.
+ *   offsets : int32 [experts + 1], not decreasing, within 0 .. slots.
+ *   slots   : rows of out (and of the residual): the most there can be.
+ *   epilogue, out : as for mmq_fold_epilogue; bias is [experts][m].
+ * A value of rows or offsets outside its range is clamped into it (the result
+ * is then meaningless, but nothing outside the arrays is touched).  The
+ * float32 arithmetic is that of the fold entry points on the kernel that the
+ * group's size takes, with the same accuracy.  Limits: experts <= 4096,
+ * tokens*k < 2^32, slots*m and experts*m*(k/256)*(block bytes) below 2^40.
+ * slots or m of 0 is an empty call.
+ */
+int mmq_fold_grouped(int format, const void *w, int64_t experts, int64_t m, int64_t k, const int8_t *q,
+                     const uint32_t *ds, int64_t tokens, const int32_t *rows, const int32_t *offsets,
+                     int64_t slots, const mmq_epilogue *epilogue, void *out, hipStream_t stream);
+
+/*
+ * moe_route - the router of mmq_fold_grouped: the `top` experts of each token
+ * by score, their softmax weights, and the slots of the grouped products.
+ *
+ *   logits  : float [n][stride] (0 = experts), experts <= 1024.  -inf and NaN
+ *             mask an expert out; +inf counts as the largest float.
+ *   top     : 1 .. min(experts, 64).
+ *   ids     : int32 [n][top] (out), the chosen experts, best first, equal
+ *             scores by lowest index; -1 where fewer experts are left (a
+ *             token whose scores are all masked has only -1).
+ *   weights : float [n][top] (out), scale * exp(l - max) / sum, the sum over
+ *             the chosen (normalize != 0) or over all unmasked experts; 0
+ *             beside -1.
+ *   slot    : int32 [n][top] (out), the slot of each choice, or -1.  Slots
+ *             are grouped by expert and in token order within one.
+ *   rows    : int32 [n*top] (out), the token of each slot; -1 behind the last.
+ *   offsets : int32 [experts + 1] (out), as mmq_fold_grouped takes them.
+ * Deterministic, no workspace.  n == 0 is an empty call (offsets too stay as
+ * they are).  MMQ_ERR_SHAPE for top outside 1 .. experts or a stride below
+ * experts; MMQ_ERR_OVERFLOW for experts above 1024, top above 64, or n*top
+ * above 2^30.
+ */
+int moe_route(const float *logits, int64_t n, int64_t experts, int64_t stride, int top, int normalize, float scale,
+              int32_t *ids, float *weights, int32_t *slot, int32_t *rows, int32_t *offsets, hipStream_t stream);
+
+/*
+ * moe_combine - the experts' outputs back in token order:
+ *
+ *   out[t][o] = residual[t][o] + sum_j weights[t][j] * y[slot[t][j]][o]
+ *
+ * in float32, over the j whose slot lies in 0 .. slots - 1 (a token without
+ * any gets its residual, or 0).
+ *
+ *   y        : float (y_f16 == 0) or binary16 [slots][m].
+ *   slot, weights : [n][top] from moe_route, top <= 64.
+ *   residual : float [n][m] or NULL; may be out itself.
+ *   out      : float [n][m] (out).
+ * n or m of 0 is an empty call.
+ */
+int moe_combine(const void *y, int y_f16, int64_t slots, int64_t m, const int32_t *slot, const float *weights,
+                int64_t n, int top, const float *residual, float *out, hipStream_t stream);
+
+/*
+ * q8_quantize_norm - the norms before and after a transformer block with the
+ * block's gate and the residual scale, fused with the q8 quantization of the
+ * next projections' input:
+ *
+ *   z  = y                                           without y_weight
+ *      = y * y_weight / sqrt(mean(y^2) + eps)        with it (the norm after the block)
+ *   r  = float32( residual_scale * x + gate * z )    the new residual stream (no gate: 1)
+ *   h  = float32( r * weight / sqrt(mean(r^2) + eps) )   (the norm before the next)
+ *   q, ds = q8_quantize_rows(h)
+ *
+ * evaluated in float64 between the roundings named, means over the k values
+ * of a token.  Without y the stream is not changed: r = x, and y_weight, gate
+ * and r must be NULL and residual_scale 1 (MMQ_ERR_NULL).
+ *
+ *   n, k     : k % 32 == 0; limits as for q8_quantize_rows, n at most 2^31 - 128
+ *              and n*1024 below 2^32.
+ *   q, ds    : as for q8_quantize_rows.
+ * Strides are elements between rows, 0 = k (gate_stride 0: one gate row for
+ * all tokens); below k they are MMQ_ERR_SHAPE, and rows must start on 16-byte
+ * boundaries (MMQ_ERR_ALIGN).  r may be x itself (same stride); otherwise
+ * outputs must not overlap inputs.
+ */
+typedef struct q8_norm {
+    const float *x;          /* [n][x_stride] residual stream */
+    const void *y;           /* [n][y_stride] block output, or NULL */
+    const float *y_weight;   /* [k], or NULL: y is not normed */
+    const float *gate;       /* [k] or [n][gate_stride], or NULL */
+    const float *weight;     /* [k] */
+    float *r;                /* [n][r_stride] (out), required with y */
+    float *h;                /* [n][k] (out), or NULL: not written */
+    int64_t x_stride, y_stride, gate_stride, r_stride;
+    float residual_scale, eps;
+    int y_f16;               /* y is binary16 (else float32) */
+} q8_norm;
+
+int q8_quantize_norm(const q8_norm *args, int64_t n, int64_t k, int8_t *q, uint32_t *ds, hipStream_t stream);
+
+/*
+ * q8_quantize_norm_tiled - q8_quantize_norm with the codes as operand tiles
+ * (k % 256 == 0), as q8_quantize_rows_tiled writes them.
+ */
+int q8_quantize_norm_tiled(const q8_norm *args, int64_t n, int64_t k, uint16_t *qt, uint32_t *ds,
+                           hipStream_t stream);
+
+/*
+ * residual_norm - q8_quantize_norm without the codes: r (with y) and h, which
+ * must not be NULL.  For the readers that take float32: a router, an output
+ * head.
+ */
+int residual_norm(const q8_norm *args, int64_t n, int64_t k, hipStream_t stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 const char *mmq_status_string(int status);

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -18,7 +19,8 @@ EXPORTS = ("q8_quantize_rows", "q8_quantize_silu_mul", "mmq_q4k_q8", "mmq_q4k_q8
            "mmq_q4k_q8_fold", "mmq_q6k_q8", "mmq_q6k_q8_fp32out", "mmq_q6k_q8_f16out", "mmq_q6k_q8_fold",
            "q4k_repack", "mmq_q4kr_q8_fp32out", "q8_quantize_rows_tiled", "mmq_q4k_q8t_fp32out",
            "mmq_q4kr_q8t_fp32out", "mmq_q6k_q8t_fp32out", "q8_quantize_silu_mul_tiled",
-           "mmq_kernel_choice", "mmq_status_string")
+           "mmq_kernel_choice", "mmq_status_string", "mmq_fold_epilogue", "mmq_fold_grouped", "moe_route",
+           "moe_combine", "q8_quantize_norm", "q8_quantize_norm_tiled", "residual_norm")
 
 # enum mmq_kernel / enum mmq_format of include/mmq.h
 KERNEL_AUTO, KERNEL_DOT4, KERNEL_FEW, KERNEL_F16, KERNEL_I8, KERNEL_NARROW, KERNEL_STREAM = 0, 1, 2, 3, 4, 5, 6
@@ -26,11 +28,41 @@ KERNEL_NAMES = {KERNEL_DOT4: "dot4", KERNEL_FEW: "few", KERNEL_F16: "f16", KERNE
                 KERNEL_NARROW: "narrow", KERNEL_STREAM: "stream"}
 (FORMAT_Q4K, FORMAT_Q4K_REPACKED, FORMAT_Q6K, FORMAT_Q4K_TILES, FORMAT_Q4K_REPACKED_TILES,
  FORMAT_Q6K_TILES) = range(6)
+_FORMAT_NAMES = {FORMAT_Q4K: "q4k", FORMAT_Q4K_REPACKED: "repacked", FORMAT_Q6K: "q6k", FORMAT_Q4K_TILES: "q4k",
+                 FORMAT_Q4K_REPACKED_TILES: "repacked", FORMAT_Q6K_TILES: "q6k"}
+_TILE_FORMATS = (FORMAT_Q4K_TILES, FORMAT_Q4K_REPACKED_TILES, FORMAT_Q6K_TILES)
+# enum mmq_activation
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 Q4K_BLOCK_BYTES, Q6K_BLOCK_BYTES, REPACK_RECORD_BYTES = 144, 210, 2368
 _MMQ_CALLS = ("mmq_q4k_q8", "mmq_q4k_q8_fp32out", "mmq_q4k_q8_f16out",
               "mmq_q6k_q8", "mmq_q6k_q8_fp32out", "mmq_q6k_q8_f16out", "mmq_q4kr_q8_fp32out",
               "mmq_q4k_q8t_fp32out", "mmq_q4kr_q8t_fp32out", "mmq_q6k_q8t_fp32out")
 _lib = None
+
+
+class Epilogue(ctypes.Structure):
+    """mmq_epilogue of include/mmq.h."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("activation", ctypes.c_int), ("residual_f16", ctypes.c_int),
+                ("out_f16", ctypes.c_int)]
+
+
+class Norm(ctypes.Structure):
+    """q8_norm of include/mmq.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("r", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64), ("residual_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("y_f16", ctypes.c_int)]
+
+
+class Routing(NamedTuple):
+    """What route() returns."""
+    ids: torch.Tensor       # int32 [n, top]
+    weights: torch.Tensor   # float32 [n, top]
+    slot: torch.Tensor      # int32 [n, top]
+    rows: torch.Tensor      # int32 [n * top]
+    offsets: torch.Tensor   # int32 [experts + 1]
 
 
 class MMQError(RuntimeError):
@@ -71,6 +103,17 @@ def load_library(path: str = LIB_PATH):
         fn.restype = ctypes.c_int
     lib.mmq_kernel_choice.argtypes = [ctypes.c_int, i64, i64, i64]
     lib.mmq_kernel_choice.restype = ctypes.c_int
+    ci, cf = ctypes.c_int, ctypes.c_float
+    for name, args in (
+            ("mmq_fold_epilogue", [ci, vp, i64, i64, vp, vp, i64, ctypes.POINTER(Epilogue), vp, vp]),
+            ("mmq_fold_grouped", [ci, vp, i64, i64, i64, vp, vp, i64, vp, vp, i64, ctypes.POINTER(Epilogue), vp, vp]),
+            ("moe_route", [vp, i64, i64, i64, ci, ci, cf, vp, vp, vp, vp, vp, vp]),
+            ("moe_combine", [vp, ci, i64, i64, vp, vp, i64, ci, vp, vp, vp]),
+            ("q8_quantize_norm", [ctypes.POINTER(Norm), i64, i64, vp, vp, vp]),
+            ("q8_quantize_norm_tiled", [ctypes.POINTER(Norm), i64, i64, vp, vp, vp]),
+            ("residual_norm", [ctypes.POINTER(Norm), i64, i64, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
     lib.mmq_status_string.argtypes = [ctypes.c_int]
     lib.mmq_status_string.restype = ctypes.c_char_p
     if path == LIB_PATH:
@@ -493,3 +536,248 @@ def repack(w: torch.Tensor, m: int, k: int):
 def fp32_repacked(wr: torch.Tensor, m: int, k: int, q: torch.Tensor, ds: torch.Tensor, out=None):
     """mmq_q4k_q8_fp32out on repacked weights: float32 [n, m]."""
     return _fold(wr, m, k, q, ds, out, "repacked", torch.float32, mmq_q4kr_q8_fp32out)
+
+
+# ------------------------------------------------- epilogue, experts, norm
+def _on(dev):
+    """Make dev the current device for a call (its stream and its kernels)."""
+    return torch.cuda.device(dev)
+
+
+def _rows(t, dtypes, n: int, k: int, name: str) -> int:
+    """The row stride of a [n, k] tensor with contiguous rows, 0 for n < 2."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda:
+        raise TypeError("%s must be a %s tensor on a HIP device" % (name, " or ".join(str(d) for d in dtypes)))
+    if t.dim() != 2 or tuple(t.shape) != (n, k):
+        raise ValueError("%s must be [%d, %d], got %s" % (name, n, k, tuple(t.shape)))
+    if t.stride(1) != 1 and k > 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if n < 2:
+        return 0
+    if t.stride(0) < k:
+        raise ValueError("%s has a row stride below %d" % (name, k))
+    return t.stride(0)
+
+
+def _vector(t, k: int, name: str):
+    _need(t, torch.float32, name)
+    if tuple(t.shape) != (k,):
+        raise ValueError("%s must be [%d], got %s" % (name, k, tuple(t.shape)))
+
+
+_F32, _FLOATS = (torch.float32,), (torch.float32, torch.float16)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h):
+    """(Norm, n, k, r, tensors) of a norm call; r: the new residual stream."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [n, k]")
+    n, k = x.shape
+    a = Norm()
+    a.x_stride = _rows(x, _F32, n, k, "x")
+    _vector(weight, k, "weight")
+    if y is None:
+        if y_weight is not None or gate is not None or r is not None or residual_scale != 1.0:
+            raise ValueError("y_weight, gate, r and residual_scale need y")
+        r = x
+    else:
+        a.y_stride = _rows(y, _FLOATS, n, k, "y")
+        a.y_f16 = y.dtype == torch.float16
+        if y_weight is not None:
+            _vector(y_weight, k, "y_weight")
+        if gate is not None:
+            if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+                _vector(gate, k, "gate")
+            else:
+                a.gate_stride = _rows(gate, _F32, n, k, "gate")
+        if r is None:
+            r = torch.empty((n, k), dtype=torch.float32, device=x.device)
+        a.r_stride = _rows(r, _F32, n, k, "r")
+        a.r = r.data_ptr()
+    if h is not None:
+        _need(h, torch.float32, "h")
+        if tuple(h.shape) != (n, k):
+            raise ValueError("h must be [%d, %d], got %s" % (n, k, tuple(h.shape)))
+    _same_device(x, weight, y, y_weight, gate, r, h)
+    a.x, a.y, a.y_weight, a.gate = _addr(x), _addr(y), _addr(y_weight), _addr(gate)
+    a.weight, a.h, a.residual_scale, a.eps = _addr(weight), _addr(h), residual_scale, eps
+    return a, n, k, r
+
+
+def quantize_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, y=None, y_weight=None, gate=None,
+                  residual_scale: float = 1.0, r=None, h=None):
+    """q8 of the normed residual stream (q8_quantize_norm): (q int8 [n, k],
+    ds int32 [n, k/32], r).  x float32 [n, k]; y float32 or binary16 [n, k];
+    gate [k] or [n, k]; r: where the new stream goes (x itself is fine), x
+    without y; h: a float32 [n, k] that gets the normed values too."""
+    a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
+    q = torch.empty((n, k), dtype=torch.int8, device=x.device)
+    ds = torch.empty((n, k // 32), dtype=torch.int32, device=x.device)
+    with _on(x.device):
+        _check("q8_quantize_norm", load_library().q8_quantize_norm(a, n, k, q.data_ptr(), ds.data_ptr(), _stream()))
+    return q, ds, r
+
+
+def quantize_norm_tiled(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, y=None, y_weight=None, gate=None,
+                        residual_scale: float = 1.0, r=None, h=None):
+    """quantize_norm with the codes as operand tiles: (qt int16
+    [tiles_elems(n, k)], ds int32 [n, k/32], r)."""
+    a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
+    qt = torch.empty(tiles_elems(n, k), dtype=torch.int16, device=x.device)
+    ds = torch.empty((n, k // 32), dtype=torch.int32, device=x.device)
+    with _on(x.device):
+        _check("q8_quantize_norm_tiled", load_library().q8_quantize_norm_tiled(
+            a, n, k, qt.data_ptr(), ds.data_ptr(), _stream()))
+    return qt, ds, r
+
+
+def norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, y=None, y_weight=None, gate=None,
+         residual_scale: float = 1.0, r=None, h=None):
+    """The normed residual stream in float32 (residual_norm): (h [n, k], r);
+    arguments as for quantize_norm."""
+    if h is None:
+        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
+    with _on(x.device):
+        _check("residual_norm", load_library().residual_norm(a, n, k, _stream()))
+    return h, r
+
+
+def _epilogue(bias, bias_shape, activation, residual, n, m, out, f16, dev):
+    """(Epilogue, out) of a call with n rows of m outputs."""
+    a = Epilogue()
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if tuple(bias.shape) != bias_shape:
+            raise ValueError("bias must be %s, got %s" % (list(bias_shape), tuple(bias.shape)))
+        a.bias = bias.data_ptr()
+    if residual is not None:
+        a.residual_stride = _rows(residual, _FLOATS, n, m, "residual")
+        a.residual_f16 = residual.dtype == torch.float16
+        a.residual = residual.data_ptr()
+    dtype = torch.float16 if f16 else torch.float32
+    if out is None:
+        out = torch.empty((n, m), dtype=dtype, device=dev)
+    a.out_stride = _rows(out, (dtype,), n, m, "out")
+    a.out_f16, a.activation = f16, activation
+    return a, out
+
+
+def fold_epilogue(fmt: int, w: torch.Tensor, m: int, k: int, q: torch.Tensor, ds: torch.Tensor, bias=None,
+                  activation: int = ACT_NONE, residual=None, out=None, f16: bool = False):
+    """act(fold + bias) + residual of a fold entry point (mmq_fold_epilogue):
+    float32 or binary16 [n, m].  fmt: FORMAT_*, q its int8 codes or operand
+    tiles; residual and out may have a row stride, and be the same tensor."""
+    if fmt not in _FORMAT_NAMES:
+        raise ValueError("unknown format %r" % (fmt,))
+    _weights(w, m, k, _FORMAT_NAMES[fmt])
+    _need(ds, torch.int32, "ds")
+    if fmt in _TILE_FORMATS:
+        _need(q, torch.int16, "q")
+        if ds.dim() != 2:
+            raise ValueError("ds must be [n, k/32]")
+        n = ds.shape[0]
+        if q.numel() != tiles_elems(n, k):
+            raise ValueError("q must hold tiles_elems(%d, %d) = %d values, got %d"
+                             % (n, k, tiles_elems(n, k), q.numel()))
+    else:
+        _need(q, torch.int8, "q")
+        n = _tokens(q, k)
+    _scale_words(ds, n, k)
+    a, out = _epilogue(bias, (m,), activation, residual, n, m, out, f16, q.device)
+    _same_device(w, q, ds, bias, residual, out)
+    with _on(q.device):
+        _check("mmq_fold_epilogue", load_library().mmq_fold_epilogue(
+            fmt, w.data_ptr(), m, k, q.data_ptr(), ds.data_ptr(), n, a, out.data_ptr(), _stream()))
+    return out
+
+
+def fold_grouped(fmt: int, w: torch.Tensor, experts: int, m: int, k: int, q: torch.Tensor, ds: torch.Tensor,
+                 offsets: torch.Tensor, rows=None, bias=None, activation: int = ACT_NONE, residual=None, out=None,
+                 f16: bool = False):
+    """Matrix products grouped by expert (mmq_fold_grouped): float32 or
+    binary16 [slots, m].  w: experts matrices of m x k (FORMAT_Q4K or
+    FORMAT_Q6K); offsets int32 [experts + 1]; rows int32 [slots], the row of q
+    of each slot, or None (slot s takes row s); bias [experts, m].  slots is
+    out's rows, else those of rows, else those of q; rows of out that belong
+    to no expert are left as they were (uninitialised in a new tensor)."""
+    if fmt not in (FORMAT_Q4K, FORMAT_Q6K):
+        raise ValueError("grouped products take FORMAT_Q4K or FORMAT_Q6K, got %r" % (fmt,))
+    if experts < 1:
+        raise ValueError("experts must be positive, got %d" % experts)
+    _mmq_sizes(m, k, 0)
+    _weights(w, experts * m, k, _FORMAT_NAMES[fmt])
+    _need(q, torch.int8, "q")
+    _need(ds, torch.int32, "ds")
+    tokens = _tokens(q, k)
+    _scale_words(ds, tokens, k)
+    _need(offsets, torch.int32, "offsets")
+    if tuple(offsets.shape) != (experts + 1,):
+        raise ValueError("offsets must be [%d], got %s" % (experts + 1, tuple(offsets.shape)))
+    if rows is not None:
+        _need(rows, torch.int32, "rows")
+        if rows.dim() != 1:
+            raise ValueError("rows must be [slots]")
+    slots = tokens if rows is None else rows.shape[0]
+    if out is not None and out.dim() == 2 and out.shape[0] < slots:
+        slots = out.shape[0]
+    a, out = _epilogue(bias, (experts, m), activation, residual, slots, m, out, f16, q.device)
+    _same_device(w, q, ds, offsets, rows, bias, residual, out)
+    with _on(q.device):
+        _check("mmq_fold_grouped", load_library().mmq_fold_grouped(
+            fmt, w.data_ptr(), experts, m, k, q.data_ptr(), ds.data_ptr(), tokens, _addr(rows), offsets.data_ptr(),
+            slots, a, out.data_ptr(), _stream()))
+    return out
+
+
+def route(logits: torch.Tensor, top: int, normalize: bool = True, scale: float = 1.0) -> Routing:
+    """The router of fold_grouped (moe_route) on float32 scores [n, experts]:
+    top experts of each token, their weights, and the slots of the grouped
+    products."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be [n, experts]")
+    n, experts = logits.shape
+    stride = _rows(logits, _F32, n, experts, "logits")
+    if not 1 <= top <= min(experts, 64):
+        raise ValueError("top must be 1 .. min(experts, 64), got %d of %d" % (top, experts))
+    dev = logits.device
+    ids = torch.empty((n, top), dtype=torch.int32, device=dev)
+    weights = torch.empty((n, top), dtype=torch.float32, device=dev)
+    slot = torch.empty((n, top), dtype=torch.int32, device=dev)
+    rows = torch.empty(n * top, dtype=torch.int32, device=dev)
+    offsets = (torch.empty if n else torch.zeros)(experts + 1, dtype=torch.int32, device=dev)
+    with _on(dev):
+        _check("moe_route", load_library().moe_route(
+            logits.data_ptr(), n, experts, stride, top, normalize, scale, ids.data_ptr(), weights.data_ptr(),
+            slot.data_ptr(), rows.data_ptr(), offsets.data_ptr(), _stream()))
+    return Routing(ids, weights, slot, rows, offsets)
+
+
+def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, residual=None, out=None):
+    """The experts' outputs back in token order (moe_combine): float32 [n, m],
+    residual + sum_j weights[:, j] * y[slot[:, j]].  y float32 or binary16
+    [slots, m]; residual may be out."""
+    if not isinstance(y, torch.Tensor) or y.dtype not in _FLOATS:
+        raise TypeError("y must be a float32 or binary16 tensor")
+    _need(y, y.dtype, "y")
+    _need(slot, torch.int32, "slot")
+    _need(weights, torch.float32, "weights")
+    if y.dim() != 2 or slot.dim() != 2 or slot.shape != weights.shape:
+        raise ValueError("need y [slots, m] and slot, weights [n, top], got %s, %s, %s"
+                         % (tuple(y.shape), tuple(slot.shape), tuple(weights.shape)))
+    (n, top), (slots, m) = slot.shape, y.shape
+    if residual is not None:
+        _need(residual, torch.float32, "residual")
+        if tuple(residual.shape) != (n, m):
+            raise ValueError("residual must be [%d, %d], got %s" % (n, m, tuple(residual.shape)))
+    out = _out_tensor(out, n, m, torch.float32, y.device)
+    _same_device(y, slot, weights, residual, out)
+    with _on(y.device):
+        _check("moe_combine", load_library().moe_combine(
+            y.data_ptr(), y.dtype == torch.float16, slots, m, slot.data_ptr(), weights.data_ptr(), n, top,
+            _addr(residual), out.data_ptr(), _stream()))
+    return out

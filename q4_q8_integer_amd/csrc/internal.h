@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "out.h"
+
 namespace mmq {
 
 // Bytes of one q4_K super-block (256 weights).
@@ -28,74 +30,75 @@ hipError_t launch_q8_quantize_silu_mul_tiled(const float* g, const float* u, int
 hipError_t launch_q8_quantize_silu_mul(const float* g, const float* u, int64_t nblocks, int8_t* q,
                                        uint32_t* ds, hipStream_t stream);
 
+// The fused norm (norm_quantize.hip): the pointers and strides of
+// include/mmq.h's q8_norm, checked.
+struct NormArgs {
+    const float* x;
+    int64_t x_stride;
+    float x_scale;            // residual scale
+    const void* y;            // null: no block output, r = x
+    int64_t y_stride;
+    int y_f16;
+    const float* y_weight;    // null: no norm of y
+    const float* gate;        // null: none
+    int64_t gate_stride;      // 0: one gate row for all tokens
+    const float* weight;
+    float eps;
+    float* r;
+    int64_t r_stride;
+    float* h;                 // null: h is not written
+};
+// Codes to q (rows), to qt (operand tiles, k % 256 == 0), or nowhere.
+hipError_t launch_norm(const NormArgs& a, int n, int k, int8_t* q, uint16_t* qt, uint32_t* ds, hipStream_t stream);
+
+// Router and combination of the matmuls grouped by expert (moe.hip).
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTop = 64;
+hipError_t launch_route(const float* logits, int64_t stride, int n, int experts, int top, bool normalize, float scale,
+                        int32_t* ids, float* weights, int32_t* slot, int32_t* rows, int32_t* offsets,
+                        hipStream_t stream);
+hipError_t launch_combine(const void* y, bool y_f16, int64_t slots, int m, const int32_t* slot, const float* weights,
+                          int n, int top, const float* residual, float* out, hipStream_t stream);
+
 // Exact int32 block dots, dots[t][o][c].
 hipError_t launch_mmq_dots(const uint8_t* w, int m, int k, const int8_t* q, int n,
                            int32_t* dots, hipStream_t stream);
-
-// Output element of the fold kernels: float32, or binary16 rounded to
-// nearest-even from the same float32 value (half_out).
-template <bool H>
-struct OutElem {
-    typedef float T;
-};
-template <>
-struct OutElem<true> {
-    typedef _Float16 T;
-};
 
 // The low 16 bits of h as a binary16 value, widened to float32 (exact).
 __device__ __forceinline__ float half_lo(uint32_t h) {
     return (float)__builtin_bit_cast(_Float16, (unsigned short)(h & 0xFFFFu));
 }
 
-template <bool H>
-__device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
-    reinterpret_cast<typename OutElem<H>::T*>(out)[i] = (typename OutElem<H>::T)v;
-}
-
-// Four consecutive outputs from index i (16-byte aligned for float32, 8 for binary16).
-template <bool H>
-__device__ __forceinline__ void store_out4(void* out, int64_t i, float a, float b, float c, float d) {
-    if (H) {
-        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(out) + i) =
-            h4{(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d};
-    } else {
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + i) = make_float4(a, b, c, d);
-    }
-}
-
 // Two-term fold, out[t][o] (float32 or binary16), int8 MFMA + three-operation epilogue.
 hipError_t launch_mmq_fp32(const uint8_t* w, int m, int k, const int8_t* q,
-                           const uint32_t* ds, int n, void* out, bool half_out, hipStream_t stream);
+                           const uint32_t* ds, int n, const Out& out, hipStream_t stream);
 
 // Two-term fold, out[t][o], binary16 MFMA on exact sc*q4 and q8 operands +
 // float32 MFMA for the min term (above 64 tokens).
 hipError_t launch_mmq_fp32_f16(const uint8_t* w, int m, int k, const int8_t* q,
-                               const uint32_t* ds, int n, void* out, bool half_out,
+                               const uint32_t* ds, int n, const Out& out,
                                hipStream_t stream);
 
 // The binary16-MFMA kernel on q4k_repack records (same arithmetic and order
 // as launch_mmq_fp32_f16, so the same float32 result bit for bit).
 hipError_t launch_mmq_fp32_f16_repacked(const uint8_t* wr, int m, int k, const int8_t* q,
-                                        const uint32_t* ds, int n, float* out, hipStream_t stream);
+                                        const uint32_t* ds, int n, const Out& out, hipStream_t stream);
 
 // The binary16-MFMA kernel with the activations as q8 operand tiles (from
 // launch_q8_quantize_tiled), on q4_K rows or q4k_repack records; the same
 // float32 result bit for bit as the int8-activation kernel.
 hipError_t launch_mmq_fp32_f16_tiles(const uint8_t* w, bool repacked, int m, int k, const uint16_t* qt,
-                                     const uint32_t* ds, int n, float* out, hipStream_t stream);
+                                     const uint32_t* ds, int n, const Out& out, hipStream_t stream);
 
 // Two-term fold, out[t][o], for n <= 64 tokens: weight-streaming int8-MFMA
 // kernel (8 waves per 16 rows, each over a slice of k).
 hipError_t launch_mmq_fp32_small(const uint8_t* w, int m, int k, const int8_t* q,
-                                 const uint32_t* ds, int n, void* out, bool half_out,
+                                 const uint32_t* ds, int n, const Out& out,
                                  hipStream_t stream);
 
 // Two-term fold, out[t][o], for 1 <= n <= kGemvMaxN tokens: 4-way int8 dot
 // products on the vector ALU, no token padding.
 hipError_t launch_mmq_fp32_gemv(const uint8_t* w, int m, int k, const int8_t* q,
-                                const uint32_t* ds, int n, void* out, bool half_out,
+                                const uint32_t* ds, int n, const Out& out,
                                 hipStream_t stream);
 constexpr int kGemvMaxN = 8;
 
@@ -103,7 +106,7 @@ constexpr int kGemvMaxN = 8;
 // kernel on that layout (1 <= n <= kGemvMaxN; w is the repacked buffer).
 hipError_t launch_q4k_repack(const uint8_t* w, int m, int k, uint8_t* wr, hipStream_t stream);
 hipError_t launch_mmq_fp32_gemv_repacked(const uint8_t* wr, int m, int k, const int8_t* q,
-                                         const uint32_t* ds, int n, void* out, bool half_out,
+                                         const uint32_t* ds, int n, const Out& out,
                                          hipStream_t stream);
 
 // Largest token count the few-token kernel takes.
@@ -113,7 +116,7 @@ constexpr int kSmallMaxN = 64;
 // MFMA on weights and tokens staged through LDS, one (row, super-block,
 // chunk half) per lane (mmq_narrow.hip).
 hipError_t launch_mmq_fp32_narrow(const uint8_t* w, int m, int k, const int8_t* q,
-                                  const uint32_t* ds, int n, void* out, bool half_out,
+                                  const uint32_t* ds, int n, const Out& out,
                                   hipStream_t stream);
 constexpr int kNarrowMaxN = 16;
 
@@ -134,20 +137,33 @@ hipError_t launch_q6k_dots(const uint8_t* w, int m, int k, const int8_t* q, int 
 
 // out[t][o] (float32 or binary16) for any n: int8 MFMA per scale group.
 hipError_t launch_q6k_i8(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                         int n, void* out, bool half_out, hipStream_t stream);
+                         int n, const Out& out, hipStream_t stream);
 
 // out[t][o] for any n: binary16 MFMA on the split exact operands sc*nibble/64
 // and sc*(hi2 - 2)/4 (one FMA per output and chunk).
 hipError_t launch_q6k_f16(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                          void* out, bool half_out, hipStream_t stream);
+                          const Out& out, hipStream_t stream);
 
 // launch_q6k_f16 with the activations as q8 operand tiles (float32 output).
 hipError_t launch_q6k_f16_tiles(const uint8_t* w, int m, int k, const uint16_t* qt, const uint32_t* ds,
-                                int n, float* out, hipStream_t stream);
+                                int n, const Out& out, hipStream_t stream);
 
 // out[t][o] for 1 <= n <= kQ6kGemvMaxN: 4-way int8 dots on the vector ALU.
 hipError_t launch_q6k_gemv(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                           int n, void* out, bool half_out, hipStream_t stream);
+                           int n, const Out& out, hipStream_t stream);
 constexpr int kQ6kGemvMaxN = 8;
+
+// The matmuls grouped by expert (group.h): the kernels above over the items
+// of the experts with g.lo .. g.hi slots.  tokens_per_item: the most slots
+// one item should hold, rounded up to what the kernel has.
+struct Groups;
+hipError_t launch_narrow_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
+                                 const OutEpi& out, int tokens_per_item, hipStream_t stream);
+hipError_t launch_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
+                              const OutEpi& out, int tokens_per_item, hipStream_t stream);
+hipError_t launch_q6k_gemv_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
+                                   const Groups& g, const OutEpi& out, int tokens_per_item, hipStream_t stream);
+hipError_t launch_q6k_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
+                                  const Groups& g, const OutEpi& out, hipStream_t stream);
 
 }  // namespace mmq

@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "../../include/mmq.h"
+#include "group.h"
 #include "internal.h"
 #include "stream.h"
 #include "q6k_device.h"
@@ -15,6 +16,8 @@ namespace {
 
 constexpr int64_t kMaxDim = 0x7fffffffLL;      // n, m
 constexpr int64_t kMaxK = 1LL << 24;
+constexpr int64_t kMaxExperts = 4096;
+constexpr int64_t kMaxRouteIds = 1LL << 30;    // n*top
 constexpr int64_t kMaxElems = 1LL << 40;       // n*k, m*k/256*144, n*m, n*m*k/32
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -58,7 +61,7 @@ int check_mmq(const void* w, int64_t m, int64_t k, const int8_t* q, int64_t n, c
     return MMQ_OK;
 }
 
-using FoldLaunch = hipError_t (*)(const uint8_t*, int, int, const int8_t*, const uint32_t*, int, void*, bool,
+using FoldLaunch = hipError_t (*)(const uint8_t*, int, int, const int8_t*, const uint32_t*, int, const mmq::Out&,
                                   hipStream_t);
 
 // HIP takes at most 2^32 - 1 work-items per grid dimension.
@@ -177,11 +180,11 @@ int hip_status(hipError_t e) {
 }
 
 // The q4_K fold entry points: same checks, same kernels, float32 or binary16
-// stores of the same float32 result.
+// stores of the same float32 result, or its epilogue.
 int fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds, int64_t n,
-               void* out, bool half_out, int kernel, hipStream_t stream) {
+               const mmq::Out& out, int kernel, hipStream_t stream) {
     bool empty = false;
-    int rc = check_mmq(w, m, k, q, n, out, &empty);
+    int rc = check_mmq(w, m, k, q, n, out.epi.p, &empty);
     if (rc != MMQ_OK || empty) return rc;
     if (!ds) return MMQ_ERR_NULL;
     if (!aligned16(ds)) return MMQ_ERR_ALIGN;
@@ -190,16 +193,15 @@ int fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const uint3
     if (rc != MMQ_OK) return rc;
     rc = check_device();
     if (rc != MMQ_OK) return rc;
-    return hip_status(launch(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out, half_out,
-                             stream));
+    return hip_status(launch(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out, stream));
 }
 
 // The fold entry points on q8 operand tiles: always the binary16-MFMA kernel
 // (the tiles are its operand layout), on q4_K rows or repacked records.
 int tiles_fold_entry(const void* w, bool repacked, int64_t m, int64_t k, const uint16_t* qt,
-                     const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
+                     const uint32_t* ds, int64_t n, const mmq::Out& out, hipStream_t stream) {
     bool empty = false;
-    int rc = check_mmq(w, m, k, reinterpret_cast<const int8_t*>(qt), n, out, &empty);
+    int rc = check_mmq(w, m, k, reinterpret_cast<const int8_t*>(qt), n, out.epi.p, &empty);
     if (rc != MMQ_OK || empty) return rc;
     if (n > kMaxDim - 127 || (n + 127) / 128 * 128 * k >= kMaxElems) return MMQ_ERR_OVERFLOW;
     if (repacked && (m + 15) / 16 * (k / 256) * mmq::kRepackRecordBytes >= kMaxElems)
@@ -236,9 +238,9 @@ int q6k_fold_launcher(int kernel, int64_t m, int64_t n, FoldLaunch* f) {
 }
 
 int q6k_fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds,
-                   int64_t n, void* out, bool half_out, int kernel, hipStream_t stream) {
+                   int64_t n, const mmq::Out& out, int kernel, hipStream_t stream) {
     bool empty = false;
-    int rc = check_mmq(w, m, k, q, n, out, &empty, mmq::kQ6kBlockBytes);
+    int rc = check_mmq(w, m, k, q, n, out.epi.p, &empty, mmq::kQ6kBlockBytes);
     if (rc != MMQ_OK || empty) return rc;
     if (!ds) return MMQ_ERR_NULL;
     if (!aligned16(ds)) return MMQ_ERR_ALIGN;
@@ -247,8 +249,173 @@ int q6k_fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const u
     if (rc != MMQ_OK) return rc;
     rc = check_device();
     if (rc != MMQ_OK) return rc;
-    return hip_status(launch(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out, half_out,
-                             stream));
+    return hip_status(launch(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out, stream));
+}
+
+// The fold entry points on repacked records.
+int repacked_fold_entry(const void* wr, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds, int64_t n,
+                        const mmq::Out& out, hipStream_t stream) {
+    bool empty = false;
+    int rc = check_mmq(wr, m, k, q, n, out.epi.p, &empty);
+    if (rc != MMQ_OK || empty) return rc;
+    if ((m + 15) / 16 * (k / 256) * mmq::kRepackRecordBytes >= kMaxElems) return MMQ_ERR_OVERFLOW;
+    if (!ds) return MMQ_ERR_NULL;
+    if (!aligned16(ds)) return MMQ_ERR_ALIGN;
+    const bool f16 = q4kr_auto_kernel(m, n) == MMQ_KERNEL_F16;
+    if (f16 ? !threads_ok((m + 127) / 128 * ((n + 63) / 64), 1024) : !threads_ok((m + 15) / 16, 256))
+        return MMQ_ERR_OVERFLOW;
+    rc = check_device();
+    if (rc != MMQ_OK) return rc;
+    if (f16)
+        return hip_status(mmq::launch_mmq_fp32_f16_repacked(static_cast<const uint8_t*>(wr), (int)m, (int)k,
+                                                            q, ds, (int)n, out, stream));
+    // Up to 8 tokens per launch; more tokens run as slices of 8 (each reads
+    // the weights again: this layout serves the few-token path).  Slice
+    // starts stay 16-byte aligned: 8 rows of q, ds and out are 8k, k/4 and
+    // 32m bytes.
+    mmq::Out part = out;
+    for (int64_t t0 = 0; t0 < n; t0 += mmq::kGemvMaxN) {
+        const int nn = (int)(n - t0 < mmq::kGemvMaxN ? n - t0 : mmq::kGemvMaxN);
+        rc = hip_status(mmq::launch_mmq_fp32_gemv_repacked(
+            static_cast<const uint8_t*>(wr), (int)m, (int)k, q + t0 * k, ds + t0 * (k / 32), nn,
+            part, stream));
+        if (rc != MMQ_OK) return rc;
+        part.epi.advance(mmq::kGemvMaxN);
+    }
+    return MMQ_OK;
+}
+
+// The q6_K fold entry points on q8 operand tiles.
+int q6k_tiles_fold_entry(const void* w, int64_t m, int64_t k, const uint16_t* qt,
+                         const uint32_t* ds, int64_t n, const mmq::Out& out, hipStream_t stream) {
+    bool empty = false;
+    int rc = check_mmq(w, m, k, reinterpret_cast<const int8_t*>(qt), n, out.epi.p, &empty, mmq::kQ6kBlockBytes);
+    if (rc != MMQ_OK || empty) return rc;
+    if (n > kMaxDim - 127 || (n + 127) / 128 * 128 * k >= kMaxElems) return MMQ_ERR_OVERFLOW;
+    if (!threads_ok((m + 127) / 128 * ((n + 127) / 128), 1024)) return MMQ_ERR_OVERFLOW;
+    if (!ds) return MMQ_ERR_NULL;
+    if (!aligned16(ds)) return MMQ_ERR_ALIGN;
+    rc = check_device();
+    if (rc != MMQ_OK) return rc;
+    return hip_status(mmq::launch_q6k_f16_tiles(static_cast<const uint8_t*>(w), (int)m, (int)k, qt, ds,
+                                                (int)n, out, stream));
+}
+
+// ------------------------------------------------------------- epilogue
+bool opt_aligned16(const void* p) { return !p || aligned16(p); }
+
+// A row stride: 0 stands for m, less than m is an error.
+int row_stride(int64_t given, int64_t m, int64_t rows, int64_t* stride) {
+    *stride = given == 0 ? m : given;
+    if (*stride < m) return MMQ_ERR_SHAPE;
+    return *stride > kMaxElems || rows > kMaxElems / (*stride > 0 ? *stride : 1) ? MMQ_ERR_OVERFLOW : MMQ_OK;
+}
+
+// The output of an epilogue call; experts: how many bias rows.
+int make_epilogue(const mmq_epilogue* e, void* out, int64_t m, int64_t rows, int64_t experts, mmq::Out* o) {
+    if (!e) return MMQ_ERR_NULL;
+    if (e->activation < MMQ_ACT_NONE || e->activation > MMQ_ACT_GELU_TANH) return MMQ_ERR_KERNEL;
+    *o = mmq::Out{};
+    o->kind = mmq::kOutEpi;
+    o->epi.p = out;
+    o->epi.bias = e->bias;
+    o->epi.res = e->residual;
+    o->epi.act = e->activation;
+    o->epi.half = e->out_f16 != 0;
+    o->epi.res_half = e->residual_f16 != 0;
+    int rc = row_stride(e->out_stride, m, rows, &o->epi.stride);
+    if (rc == MMQ_OK) rc = row_stride(e->residual ? e->residual_stride : 0, m, rows, &o->epi.res_stride);
+    if (rc != MMQ_OK) return rc;
+    if (!opt_aligned16(e->bias) || !opt_aligned16(e->residual)) return MMQ_ERR_ALIGN;
+    o->epi.vec4 = (o->epi.stride & 3) == 0 && (!e->residual || (o->epi.res_stride & 3) == 0) &&
+                  (!e->bias || experts == 1 || (m & 3) == 0);
+    return MMQ_OK;
+}
+
+// -------------------------------------------------------------- grouped
+// The experts with up to kFewSlots slots run on the few-token kernels, those
+// with more on the binary16-MFMA kernels; which are which only the device
+// knows, so both are launched unless the slots cannot reach the border.
+int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t k, const int8_t* q,
+                  const uint32_t* ds, int64_t tokens, const int32_t* rows, const int32_t* offsets, int64_t slots,
+                  const mmq_epilogue* epilogue, void* out, hipStream_t stream) {
+    if (format != MMQ_FORMAT_Q4K && format != MMQ_FORMAT_Q6K) return MMQ_ERR_KERNEL;
+    const bool q6k = format == MMQ_FORMAT_Q6K;
+    const int64_t block = q6k ? mmq::kQ6kBlockBytes : mmq::kBlockBytes;
+    if (experts <= 0 || tokens < 0 || slots < 0 || m < 0 || k <= 0 || (k & 255) != 0) return MMQ_ERR_SHAPE;
+    if (experts > kMaxExperts || tokens > kMaxDim || slots > kMaxDim || m > kMaxDim || k > kMaxK)
+        return MMQ_ERR_OVERFLOW;
+    if (slots > 0 && (tokens == 0 || (!rows && tokens < slots))) return MMQ_ERR_SHAPE;
+    if (tokens * k > 0xFFFFFFFFLL || m * (k / 256) * block >= kMaxElems / experts || slots * m >= kMaxElems)
+        return MMQ_ERR_OVERFLOW;
+    mmq::Out o;
+    int rc = make_epilogue(epilogue, out, m, slots, experts, &o);
+    if (rc != MMQ_OK) return rc;
+    if (slots == 0 || m == 0) return MMQ_OK;
+    if (!w || !q || !ds || !offsets || !out) return MMQ_ERR_NULL;
+    if (!aligned16(w) || !aligned16(q) || !aligned16(ds) || !aligned16(offsets) || !opt_aligned16(rows) ||
+        !aligned16(out))
+        return MMQ_ERR_ALIGN;
+    if (experts > 1 && (m * (k / 256) * block) % 16 != 0) return MMQ_ERR_ALIGN;   // every expert's first row
+    const int64_t few = q6k ? mmq::kQ6kGemvMaxN : mmq::kNarrowMaxN;
+    // tiles are numbered in 32 bits; one slot per item and 16 rows per tile is the most there can be
+    if (mmq::most_items(experts, slots, 1, slots, 1) * ((m + 15) / 16) > kMaxDim) return MMQ_ERR_OVERFLOW;
+    rc = check_device();
+    if (rc != MMQ_OK) return rc;
+    mmq::Groups g{offsets, rows, (int)experts, (int)slots, (int)tokens, 1, (int)few};
+    const int64_t mean = slots / experts;
+    const uint8_t* wb = static_cast<const uint8_t*>(w);
+    const int per = slots <= 4 || mean < 1 ? 4 : mean < 4 ? 8 : 16;
+    rc = hip_status(q6k ? mmq::launch_q6k_gemv_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream)
+                        : mmq::launch_narrow_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream));
+    if (rc != MMQ_OK || slots <= few) return rc;
+    g.lo = (int)few + 1;
+    g.hi = (int)slots;
+    return hip_status(q6k ? mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream)
+                          : mmq::launch_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, mean < 96 ? 64 : 128, stream));
+}
+
+// ----------------------------------------------------------------- norm
+int norm_entry(const q8_norm* a, int64_t n, int64_t k, int8_t* q, uint16_t* qt, uint32_t* ds, bool codes, bool tiles,
+               hipStream_t stream) {
+    if (n < 0 || k <= 0 || (k & (tiles ? 255 : 31)) != 0) return MMQ_ERR_SHAPE;
+    if (n > kMaxDim - 127 || k > kMaxK || (n + 127) / 128 * 128 * k >= kMaxElems) return MMQ_ERR_OVERFLOW;
+    if (!threads_ok((n + 127) / 128 * 128, 1024)) return MMQ_ERR_OVERFLOW;   // a workgroup per row
+    if (n == 0) return MMQ_OK;
+    if (!a || !a->x || !a->weight) return MMQ_ERR_NULL;
+    if (codes && ((tiles ? (const void*)qt : (const void*)q) == nullptr || !ds)) return MMQ_ERR_NULL;
+    if (!codes && !a->h) return MMQ_ERR_NULL;
+    // the stream needs a place where it changes; without y it does not
+    if (a->y ? !a->r : (a->r || a->y_weight || a->gate || a->residual_scale != 1.0f)) return MMQ_ERR_NULL;
+    mmq::NormArgs v{};
+    int rc = row_stride(a->x_stride, k, n, &v.x_stride);
+    if (rc == MMQ_OK && a->y) rc = row_stride(a->y_stride, k, n, &v.y_stride);
+    if (rc == MMQ_OK && a->y) rc = row_stride(a->r_stride, k, n, &v.r_stride);
+    if (rc != MMQ_OK) return rc;
+    if (a->gate && a->gate_stride != 0) {
+        rc = row_stride(a->gate_stride, k, n, &v.gate_stride);
+        if (rc != MMQ_OK) return rc;
+    }
+    if (!aligned16(a->x) || !opt_aligned16(a->y) || !opt_aligned16(a->y_weight) || !opt_aligned16(a->gate) ||
+        !aligned16(a->weight) || !opt_aligned16(a->r) || !opt_aligned16(a->h) || !opt_aligned16(q) ||
+        !opt_aligned16(qt) || !opt_aligned16(ds))
+        return MMQ_ERR_ALIGN;
+    // rows start on 16-byte boundaries
+    if ((v.x_stride & 3) || (v.y_stride & (a->y_f16 ? 7 : 3)) || (v.r_stride & 3) || (v.gate_stride & 3))
+        return MMQ_ERR_ALIGN;
+    v.x = a->x;
+    v.x_scale = a->residual_scale;
+    v.y = a->y;
+    v.y_f16 = a->y_f16 != 0;
+    v.y_weight = a->y_weight;
+    v.gate = a->gate;
+    v.weight = a->weight;
+    v.eps = a->eps;
+    v.r = a->r;
+    v.h = a->h;
+    const int dev = check_device();
+    if (dev != MMQ_OK) return dev;
+    return hip_status(mmq::launch_norm(v, (int)n, (int)k, q, qt, ds, stream));
 }
 
 }  // namespace
@@ -324,17 +491,17 @@ int mmq_q4k_q8(const void* w, int64_t m, int64_t k, const int8_t* q, const uint3
 
 int mmq_q4k_q8_fp32out(const void* w, int64_t m, int64_t k, const int8_t* q,
                        const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
-    return fold_entry(w, m, k, q, ds, n, out, false, MMQ_KERNEL_AUTO, stream);
+    return fold_entry(w, m, k, q, ds, n, mmq::Out::plain(out, m, false), MMQ_KERNEL_AUTO, stream);
 }
 
 int mmq_q4k_q8_f16out(const void* w, int64_t m, int64_t k, const int8_t* q,
                       const uint32_t* ds, int64_t n, uint16_t* out, hipStream_t stream) {
-    return fold_entry(w, m, k, q, ds, n, out, true, MMQ_KERNEL_AUTO, stream);
+    return fold_entry(w, m, k, q, ds, n, mmq::Out::plain(out, m, true), MMQ_KERNEL_AUTO, stream);
 }
 
 int mmq_q4k_q8_fold(const void* w, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds, int64_t n,
                     void* out, int out_f16, int kernel, hipStream_t stream) {
-    return fold_entry(w, m, k, q, ds, n, out, out_f16 != 0, kernel, stream);
+    return fold_entry(w, m, k, q, ds, n, mmq::Out::plain(out, m, out_f16 != 0), kernel, stream);
 }
 
 int mmq_q6k_q8(const void* w, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds,
@@ -354,17 +521,17 @@ int mmq_q6k_q8(const void* w, int64_t m, int64_t k, const int8_t* q, const uint3
 
 int mmq_q6k_q8_fp32out(const void* w, int64_t m, int64_t k, const int8_t* q,
                        const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
-    return q6k_fold_entry(w, m, k, q, ds, n, out, false, MMQ_KERNEL_AUTO, stream);
+    return q6k_fold_entry(w, m, k, q, ds, n, mmq::Out::plain(out, m, false), MMQ_KERNEL_AUTO, stream);
 }
 
 int mmq_q6k_q8_f16out(const void* w, int64_t m, int64_t k, const int8_t* q,
                       const uint32_t* ds, int64_t n, uint16_t* out, hipStream_t stream) {
-    return q6k_fold_entry(w, m, k, q, ds, n, out, true, MMQ_KERNEL_AUTO, stream);
+    return q6k_fold_entry(w, m, k, q, ds, n, mmq::Out::plain(out, m, true), MMQ_KERNEL_AUTO, stream);
 }
 
 int mmq_q6k_q8_fold(const void* w, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds, int64_t n,
                     void* out, int out_f16, int kernel, hipStream_t stream) {
-    return q6k_fold_entry(w, m, k, q, ds, n, out, out_f16 != 0, kernel, stream);
+    return q6k_fold_entry(w, m, k, q, ds, n, mmq::Out::plain(out, m, out_f16 != 0), kernel, stream);
 }
 
 int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n) {
@@ -397,57 +564,95 @@ int q4k_repack(const void* w, int64_t m, int64_t k, void* wr, hipStream_t stream
 
 int mmq_q4kr_q8_fp32out(const void* wr, int64_t m, int64_t k, const int8_t* q,
                         const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
-    bool empty = false;
-    int rc = check_mmq(wr, m, k, q, n, out, &empty);
-    if (rc != MMQ_OK || empty) return rc;
-    if ((m + 15) / 16 * (k / 256) * mmq::kRepackRecordBytes >= kMaxElems) return MMQ_ERR_OVERFLOW;
-    if (!ds) return MMQ_ERR_NULL;
-    if (!aligned16(ds)) return MMQ_ERR_ALIGN;
-    const bool f16 = q4kr_auto_kernel(m, n) == MMQ_KERNEL_F16;
-    if (f16 ? !threads_ok((m + 127) / 128 * ((n + 63) / 64), 1024) : !threads_ok((m + 15) / 16, 256))
-        return MMQ_ERR_OVERFLOW;
-    rc = check_device();
-    if (rc != MMQ_OK) return rc;
-    if (f16)
-        return hip_status(mmq::launch_mmq_fp32_f16_repacked(static_cast<const uint8_t*>(wr), (int)m, (int)k,
-                                                            q, ds, (int)n, out, stream));
-    // Up to 8 tokens per launch; more tokens run as slices of 8 (each reads
-    // the weights again: this layout serves the few-token path).  Slice
-    // starts stay 16-byte aligned: 8 rows of q, ds and out are 8k, k/4 and
-    // 32m bytes.
-    for (int64_t t0 = 0; t0 < n; t0 += mmq::kGemvMaxN) {
-        const int nn = (int)(n - t0 < mmq::kGemvMaxN ? n - t0 : mmq::kGemvMaxN);
-        rc = hip_status(mmq::launch_mmq_fp32_gemv_repacked(
-            static_cast<const uint8_t*>(wr), (int)m, (int)k, q + t0 * k, ds + t0 * (k / 32), nn,
-            out + t0 * m, false, stream));
-        if (rc != MMQ_OK) return rc;
-    }
-    return MMQ_OK;
+    return repacked_fold_entry(wr, m, k, q, ds, n, mmq::Out::plain(out, m, false), stream);
 }
 
 int mmq_q4k_q8t_fp32out(const void* w, int64_t m, int64_t k, const uint16_t* qt,
                         const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
-    return tiles_fold_entry(w, false, m, k, qt, ds, n, out, stream);
+    return tiles_fold_entry(w, false, m, k, qt, ds, n, mmq::Out::plain(out, m, false), stream);
 }
 
 int mmq_q4kr_q8t_fp32out(const void* wr, int64_t m, int64_t k, const uint16_t* qt,
                          const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
-    return tiles_fold_entry(wr, true, m, k, qt, ds, n, out, stream);
+    return tiles_fold_entry(wr, true, m, k, qt, ds, n, mmq::Out::plain(out, m, false), stream);
 }
 
 int mmq_q6k_q8t_fp32out(const void* w, int64_t m, int64_t k, const uint16_t* qt,
                         const uint32_t* ds, int64_t n, float* out, hipStream_t stream) {
-    bool empty = false;
-    int rc = check_mmq(w, m, k, reinterpret_cast<const int8_t*>(qt), n, out, &empty, mmq::kQ6kBlockBytes);
-    if (rc != MMQ_OK || empty) return rc;
-    if (n > kMaxDim - 127 || (n + 127) / 128 * 128 * k >= kMaxElems) return MMQ_ERR_OVERFLOW;
-    if (!threads_ok((m + 127) / 128 * ((n + 127) / 128), 1024)) return MMQ_ERR_OVERFLOW;
-    if (!ds) return MMQ_ERR_NULL;
-    if (!aligned16(ds)) return MMQ_ERR_ALIGN;
-    rc = check_device();
+    return q6k_tiles_fold_entry(w, m, k, qt, ds, n, mmq::Out::plain(out, m, false), stream);
+}
+
+int q8_quantize_norm(const q8_norm* a, int64_t n, int64_t k, int8_t* q, uint32_t* ds, hipStream_t stream) {
+    return norm_entry(a, n, k, q, nullptr, ds, true, false, stream);
+}
+
+int q8_quantize_norm_tiled(const q8_norm* a, int64_t n, int64_t k, uint16_t* qt, uint32_t* ds, hipStream_t stream) {
+    return norm_entry(a, n, k, nullptr, qt, ds, true, true, stream);
+}
+
+int residual_norm(const q8_norm* a, int64_t n, int64_t k, hipStream_t stream) {
+    return norm_entry(a, n, k, nullptr, nullptr, nullptr, false, false, stream);
+}
+
+int mmq_fold_epilogue(int format, const void* w, int64_t m, int64_t k, const void* q, const uint32_t* ds, int64_t n,
+                      const mmq_epilogue* epilogue, void* out, hipStream_t stream) {
+    if (n < 0 || m < 0) return MMQ_ERR_SHAPE;
+    if (n > kMaxDim || m > kMaxDim) return MMQ_ERR_OVERFLOW;
+    mmq::Out o;
+    const int rc = make_epilogue(epilogue, out, m, n, 1, &o);
     if (rc != MMQ_OK) return rc;
-    return hip_status(mmq::launch_q6k_f16_tiles(static_cast<const uint8_t*>(w), (int)m, (int)k, qt, ds,
-                                                (int)n, out, stream));
+    const int8_t* codes = static_cast<const int8_t*>(q);
+    const uint16_t* tiles = static_cast<const uint16_t*>(q);
+    switch (format) {
+        case MMQ_FORMAT_Q4K: return fold_entry(w, m, k, codes, ds, n, o, MMQ_KERNEL_AUTO, stream);
+        case MMQ_FORMAT_Q4K_REPACKED: return repacked_fold_entry(w, m, k, codes, ds, n, o, stream);
+        case MMQ_FORMAT_Q6K: return q6k_fold_entry(w, m, k, codes, ds, n, o, MMQ_KERNEL_AUTO, stream);
+        case MMQ_FORMAT_Q4K_TILES: return tiles_fold_entry(w, false, m, k, tiles, ds, n, o, stream);
+        case MMQ_FORMAT_Q4K_REPACKED_TILES: return tiles_fold_entry(w, true, m, k, tiles, ds, n, o, stream);
+        case MMQ_FORMAT_Q6K_TILES: return q6k_tiles_fold_entry(w, m, k, tiles, ds, n, o, stream);
+        default: return MMQ_ERR_KERNEL;
+    }
+}
+
+int mmq_fold_grouped(int format, const void* w, int64_t experts, int64_t m, int64_t k, const int8_t* q,
+                     const uint32_t* ds, int64_t tokens, const int32_t* rows, const int32_t* offsets, int64_t slots,
+                     const mmq_epilogue* epilogue, void* out, hipStream_t stream) {
+    return grouped_entry(format, w, experts, m, k, q, ds, tokens, rows, offsets, slots, epilogue, out, stream);
+}
+
+int moe_route(const float* logits, int64_t n, int64_t experts, int64_t stride, int top, int normalize, float scale,
+              int32_t* ids, float* weights, int32_t* slot, int32_t* rows, int32_t* offsets, hipStream_t stream) {
+    if (n < 0 || experts <= 0 || top <= 0 || top > experts) return MMQ_ERR_SHAPE;
+    if (experts > mmq::kRouteMaxExperts || top > mmq::kRouteMaxTop) return MMQ_ERR_OVERFLOW;
+    int64_t s = 0;
+    const int rc = row_stride(stride, experts, n, &s);
+    if (rc != MMQ_OK) return rc;
+    if (n > kMaxDim || n * top > kMaxRouteIds || !threads_ok(n, 64)) return MMQ_ERR_OVERFLOW;   // a wave per token
+    if (n == 0) return MMQ_OK;
+    if (!logits || !ids || !weights || !slot || !rows || !offsets) return MMQ_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(slot) || !aligned16(rows) ||
+        !aligned16(offsets))
+        return MMQ_ERR_ALIGN;
+    const int dev = check_device();
+    if (dev != MMQ_OK) return dev;
+    return hip_status(mmq::launch_route(logits, s, (int)n, (int)experts, top, normalize != 0, scale, ids, weights, slot,
+                                        rows, offsets, stream));
+}
+
+int moe_combine(const void* y, int y_f16, int64_t slots, int64_t m, const int32_t* slot, const float* weights,
+                int64_t n, int top, const float* residual, float* out, hipStream_t stream) {
+    if (slots < 0 || n < 0 || m < 0 || top <= 0) return MMQ_ERR_SHAPE;
+    if (slots > kMaxDim || n > kMaxDim || m > kMaxDim || top > mmq::kRouteMaxTop) return MMQ_ERR_OVERFLOW;
+    if (slots * m >= kMaxElems || n * m >= kMaxElems || n * top > kMaxRouteIds) return MMQ_ERR_OVERFLOW;
+    if (!threads_ok(n * ((m + 255) / 256), 256)) return MMQ_ERR_OVERFLOW;
+    if (n == 0 || m == 0) return MMQ_OK;
+    if ((slots > 0 && !y) || !slot || !weights || !out) return MMQ_ERR_NULL;
+    if (!opt_aligned16(y) || !aligned16(slot) || !aligned16(weights) || !opt_aligned16(residual) || !aligned16(out))
+        return MMQ_ERR_ALIGN;
+    const int dev = check_device();
+    if (dev != MMQ_OK) return dev;
+    return hip_status(mmq::launch_combine(y, y_f16 != 0, slots, (int)m, slot, weights, (int)n, top, residual, out,
+                                          stream));
 }
 
 const char* mmq_status_string(int status) {
@@ -459,7 +664,7 @@ const char* mmq_status_string(int status) {
         case MMQ_ERR_OVERFLOW: return "MMQ_ERR_OVERFLOW: size beyond the kernels' index range";
         case MMQ_ERR_DEVICE: return "MMQ_ERR_DEVICE: no HIP device, or the current device is not gfx950";
         case MMQ_ERR_HIP: return "MMQ_ERR_HIP: the HIP runtime reported a launch error";
-        case MMQ_ERR_KERNEL: return "MMQ_ERR_KERNEL: unknown kernel or format, or a kernel outside its token range";
+        case MMQ_ERR_KERNEL: return "MMQ_ERR_KERNEL: unknown kernel, format or activation, or a kernel outside its token range";
         default: return "unknown mmq status";
     }
 }

@@ -39,7 +39,10 @@
 // already binary16 and already in the B slot order: the producers copy each
 // stage's 32 KiB block into LDS with buffer_load ... lds and convert weights
 // only.
+#include <algorithm>
+
 #include "f16_operand.h"
+#include "group.h"
 #include "internal.h"
 #include "kquant_device.h"
 
@@ -126,13 +129,15 @@ struct Src {
 // leave CUs idle); the LDS stage keeps its BN-token size.
 // REP: w holds q4k_repack records (16-row tiles, one 2368-byte record per
 // tile and super-block) instead of q4_K rows.
-template <int TB, bool REP, bool QT>
+// The tile's tokens are rows src.row(0 .. toks - 1) of q and ds, which hold
+// q_rows rows (a plain call passes its tile's first token's q and ds).
+template <int TB, bool REP, bool QT, class Grp>
 __device__ __forceinline__ void init_src(Src& p, const uint8_t* __restrict__ w,
                                          const int8_t* __restrict__ q,
-                                         const uint32_t* __restrict__ ds, int pt, int row0,
-                                         int tok0, int M, int N, int K) {
+                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& src, uint32_t q_rows,
+                                         int pt, int row0, int tok0, int M, int K) {
     const int S = K >> 8, C = K >> 5;
-    const int rows = min(BM, M - row0), toks = min(TB, N - tok0);
+    const int rows = min(BM, M - row0);
     const int row_bytes = S * kBlockBytes;
     // repacked: the workgroup's 16-row tiles (up to 8), S records each
     const int tile_bytes = S * kRepackRecordBytes, ntile = (rows + 15) >> 4;
@@ -142,10 +147,9 @@ __device__ __forceinline__ void init_src(Src& p, const uint8_t* __restrict__ w,
     else
         p.w = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(w + (int64_t)row0 * row_bytes), 0,
                                                 rows * row_bytes, kBufferFlags);
-    p.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(q + (int64_t)tok0 * K), 0,
-                                            (int)((uint32_t)toks * (uint32_t)K), kBufferFlags);   // up to 2^31 bytes
-    p.ds = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(ds + (int64_t)tok0 * C), 0,
-                                             toks * C * 4, kBufferFlags);
+    p.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(q), 0, (int)(q_rows * (uint32_t)K), kBufferFlags);
+    p.ds = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(ds), 0, (int)(q_rows * (uint32_t)(C * 4)),
+                                             kBufferFlags);
     if (QT) {
         p.qt = reinterpret_cast<const uint16_t*>(q) + (int64_t)(tok0 >> 7) * (K >> 7) * (kQtBlockBytes / 2);
         p.qhalf = (tok0 >> 6) & 1;
@@ -172,7 +176,7 @@ __device__ __forceinline__ void init_src(Src& p, const uint8_t* __restrict__ w,
         const int i = pt + rr * PT;
         const int tok = (i & 15) | ((i >> 7) << 4);
         const int j = (i >> 4) & 7, cl = j >> 1, gg = j & 1;
-        p.y[rr] = min(tok, toks - 1) * K + 32 * cl + 16 * gg;
+        p.y[rr] = (int)(src.row(tok) * (uint32_t)K + 32 * cl + 16 * gg);
     }
 #pragma unroll
     for (int rr = 0; rr < SPC; ++rr) {
@@ -182,7 +186,7 @@ __device__ __forceinline__ void init_src(Src& p, const uint8_t* __restrict__ w,
         // hold a word (the others re-read the last one and store nothing)
         const int i = TB == BN ? pt + rr * PT : min(pt + rr * PT, TB * 4 - 1);
         const int tok = i >> 2, cl = i & 3;
-        p.word[rr] = (min(tok, toks - 1) * C + cl) * 4;
+        p.word[rr] = (int)((src.row(tok) * (uint32_t)C + cl) * 4);
     }
 }
 
@@ -441,20 +445,15 @@ constexpr int kGroup = 256;
 // work on stage s, the producers fill stage s+1 (their global loads run one
 // stage further ahead in registers, two with int8 codes).  One workgroup
 // barrier per stage.
-template <int TB, bool H, bool REP, bool QT, bool BIG>
-__global__ __launch_bounds__(NT) void mmq_f16_kernel(const uint8_t* __restrict__ w,
-                                                     const int8_t* __restrict__ q,
-                                                     const uint32_t* __restrict__ ds,
-                                                     int M, int N, int K, int tiles_m, int tile_m0,
-                                                     void* __restrict__ out) {
-    __shared__ Stage stage[2];
-    __shared__ StageB stage_b[2];
-
+//
+// f16_tile is one tile: rows row0 .. row0 + 127, and the N - tok0 (at most TB)
+// tokens of src, written as tokens tok0 .. of out.
+template <int TB, class O, bool REP, bool QT, bool BIG, class Grp>
+__device__ __forceinline__ void f16_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
+                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& tokens,
+                                         uint32_t q_rows, int M, int N, int K, int row0, int tok0, const O& out,
+                                         Stage (&stage)[2], StageB (&stage_b)[2]) {
     const int tid = threadIdx.x;
-    // row tiles tile_m0 .. tile_m0 + tiles_m - 1 of the M rows (a launch may
-    // cover part of them), token tiles of TB
-    const int bm = tile_m0 + blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
-    const int row0 = bm * BM, tok0 = bn * TB;
     const int stages = K >> 7;
 
     if (tid >= CT) {
@@ -466,7 +465,7 @@ __global__ __launch_bounds__(NT) void mmq_f16_kernel(const uint8_t* __restrict__
         // final stage), which lets the compiler wait only for the oldest set.
         const int pt = tid - CT;
         Src src;
-        init_src<TB, REP, QT>(src, w, q, ds, pt, row0, tok0, M, N, K);
+        init_src<TB, REP, QT>(src, w, q, ds, tokens, q_rows, pt, row0, tok0, M, K);
         Raw ra, rb;
         if constexpr (!QT) {
             // Three sets: loads run two stages ahead of the conversion (the
@@ -566,7 +565,7 @@ __global__ __launch_bounds__(NT) void mmq_f16_kernel(const uint8_t* __restrict__
 #pragma unroll
             for (int b = 0; b < NTW; ++b) acc[a][b] += acc2[a][b];
 
-    const bool vec = (M & 3) == 0;
+    const bool vec = out.vec();
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -576,17 +575,47 @@ __global__ __launch_bounds__(NT) void mmq_f16_kernel(const uint8_t* __restrict__
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 const int o = row0 + wm * 32 * RT + rt * 32 + 8 * jj + 4 * g;
-                const int64_t idx = (int64_t)tok * M + o;
                 if (vec && o + 3 < M) {
-                    store_out4<H>(out, idx, acc[rt][nt][4 * jj], acc[rt][nt][4 * jj + 1],
-                                  acc[rt][nt][4 * jj + 2], acc[rt][nt][4 * jj + 3]);
+                    out.put4(tok, o, acc[rt][nt][4 * jj], acc[rt][nt][4 * jj + 1],
+                             acc[rt][nt][4 * jj + 2], acc[rt][nt][4 * jj + 3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (o + i < M) store_out<H>(out, idx + i, acc[rt][nt][4 * jj + i]);
+                        if (o + i < M) out.put(tok, o + i, acc[rt][nt][4 * jj + i]);
                 }
             }
         }
+}
+
+template <int TB, class O, bool REP, bool QT, bool BIG, class Grp>
+__global__ __launch_bounds__(NT) void mmq_f16_kernel(const uint8_t* __restrict__ w,
+                                                     const int8_t* __restrict__ q,
+                                                     const uint32_t* __restrict__ ds,
+                                                     int M, int N, int K, int tiles_m, int tile_m0,
+                                                     O out, Grp grp) {
+    __shared__ Stage stage[2];
+    __shared__ StageB stage_b[2];
+    if constexpr (!Grp::kOn) {
+        // row tiles tile_m0 .. tile_m0 + tiles_m - 1 of the M rows (a launch may
+        // cover part of them), token tiles of TB
+        const int bm = tile_m0 + blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
+        const int tok0 = bn * TB, toks = min(TB, N - tok0);
+        f16_tile<TB, O, REP, QT, BIG, Grp>(w, QT ? q : q + (int64_t)tok0 * K, ds + (int64_t)tok0 * (K >> 5),
+                                           TokenRows<Grp>(grp, Item{}, toks), (uint32_t)toks, M, N, K, bm * BM, tok0,
+                                           out, stage, stage_b);
+    } else {
+        // tile i: row tile i % tiles_m of item i / tiles_m
+        for (int i = blockIdx.x;; i += gridDim.x) {
+            const Item it = find_item<TB>(grp, i / tiles_m);
+            if (!it.valid) return;   // the same for every wave
+            O o = out;
+            o.advance(it.start);
+            if (o.bias) o.bias += (int64_t)it.expert * M;
+            f16_tile<TB, O, REP, QT, BIG, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kBlockBytes, q, ds,
+                                               TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, it.count, K,
+                                               i % tiles_m * BM, 0, o, stage, stage_b);
+        }
+    }
 }
 
 }  // namespace
@@ -627,55 +656,73 @@ static TileShape tile_shape(int m, int n) {
 
 // The kernel instance for a launch: token tile, output type, weight layout,
 // activation format, and whether k has more than kGroup super-blocks.
-template <bool H, bool REP, bool QT>
+template <class O, bool REP, bool QT>
 static const void* pick_kernel(bool half_tiles, bool big) {
     if (half_tiles)
-        return big ? (const void*)mmq_f16_kernel<BN / 2, H, REP, QT, true>
-                   : (const void*)mmq_f16_kernel<BN / 2, H, REP, QT, false>;
-    return big ? (const void*)mmq_f16_kernel<BN, H, REP, QT, true>
-               : (const void*)mmq_f16_kernel<BN, H, REP, QT, false>;
+        return big ? (const void*)mmq_f16_kernel<BN / 2, O, REP, QT, true, NoGroups>
+                   : (const void*)mmq_f16_kernel<BN / 2, O, REP, QT, false, NoGroups>;
+    return big ? (const void*)mmq_f16_kernel<BN, O, REP, QT, true, NoGroups>
+               : (const void*)mmq_f16_kernel<BN, O, REP, QT, false, NoGroups>;
 }
 
 static hipError_t launch_part(const void* f, const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                               int n, void* out, int tiles_m, int tile_m0, int tb, hipStream_t stream) {
+    NoGroups none;
     void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k,
-                    (void*)&tiles_m, (void*)&tile_m0, (void*)&out};
+                    (void*)&tiles_m, (void*)&tile_m0, out, (void*)&none};
     const int64_t tiles = (int64_t)tiles_m * ((n + tb - 1) / tb);
     return hipLaunchKernel(f, dim3((unsigned)tiles), dim3(NT), args, 0, stream);
 }
 
 // One launch, or the two parts of a row split, on the caller's stream.
-template <bool H, bool REP, bool QT>
-static hipError_t launch(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, void* out,
+template <bool REP, bool QT, class O>
+static hipError_t launch(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, O out,
                          hipStream_t stream) {
     const TileShape t = tile_shape(m, n);
     const bool big = (k >> 8) > kGroup;
     if (t.split_m == 0)
-        return launch_part(pick_kernel<H, REP, QT>(t.half, big), w, m, k, q, ds, n, out, t.tiles_m, 0,
+        return launch_part(pick_kernel<O, REP, QT>(t.half, big), w, m, k, q, ds, n, &out, t.tiles_m, 0,
                            t.half ? BN / 2 : BN, stream);
-    const hipError_t e = launch_part(pick_kernel<H, REP, QT>(false, big), w, m, k, q, ds, n, out, t.split_m, 0,
+    const hipError_t e = launch_part(pick_kernel<O, REP, QT>(false, big), w, m, k, q, ds, n, &out, t.split_m, 0,
                                      BN, stream);
     if (e != hipSuccess) return e;
-    return launch_part(pick_kernel<H, REP, QT>(true, big), w, m, k, q, ds, n, out, t.tiles_m - t.split_m,
+    return launch_part(pick_kernel<O, REP, QT>(true, big), w, m, k, q, ds, n, &out, t.tiles_m - t.split_m,
                        t.split_m, BN / 2, stream);
 }
 
 hipError_t launch_mmq_fp32_f16(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                               int n, void* out, bool half_out, hipStream_t stream) {
-    return half_out ? launch<true, false, false>(w, m, k, q, ds, n, out, stream)
-                    : launch<false, false, false>(w, m, k, q, ds, n, out, stream);
+                               int n, const Out& out, hipStream_t stream) {
+    return with_out(out, [&](auto o) { return launch<false, false>(w, m, k, q, ds, n, o, stream); });
 }
 
 hipError_t launch_mmq_fp32_f16_repacked(const uint8_t* wr, int m, int k, const int8_t* q,
-                                        const uint32_t* ds, int n, float* out, hipStream_t stream) {
-    return launch<false, true, false>(wr, m, k, q, ds, n, out, stream);
+                                        const uint32_t* ds, int n, const Out& out, hipStream_t stream) {
+    return with_out_f32(out, [&](auto o) { return launch<true, false>(wr, m, k, q, ds, n, o, stream); });
 }
 
 hipError_t launch_mmq_fp32_f16_tiles(const uint8_t* w, bool repacked, int m, int k, const uint16_t* qt,
-                                     const uint32_t* ds, int n, float* out, hipStream_t stream) {
+                                     const uint32_t* ds, int n, const Out& out, hipStream_t stream) {
     const int8_t* q = reinterpret_cast<const int8_t*>(qt);
-    return repacked ? launch<false, true, true>(w, m, k, q, ds, n, out, stream)
-                    : launch<false, false, true>(w, m, k, q, ds, n, out, stream);
+    return with_out_f32(out, [&](auto o) {
+        return repacked ? launch<true, true>(w, m, k, q, ds, n, o, stream)
+                        : launch<false, true>(w, m, k, q, ds, n, o, stream);
+    });
+}
+
+hipError_t launch_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
+                              const OutEpi& out, int tokens_per_item, hipStream_t stream) {
+    const int tb = tokens_per_item <= 64 ? 64 : 128;
+    int tiles_m = (m + BM - 1) / BM, n = 0, tile_m0 = 0;
+    // a workgroup fills a CU
+    const int64_t tiles = most_items(g.experts, g.slots, g.lo, g.hi, tb) * tiles_m;
+    const bool big = (k >> 8) > kGroup;
+    const void* f = tb == 64 ? (big ? (const void*)mmq_f16_kernel<BN / 2, OutEpi, false, false, true, Groups>
+                                    : (const void*)mmq_f16_kernel<BN / 2, OutEpi, false, false, false, Groups>)
+                             : (big ? (const void*)mmq_f16_kernel<BN, OutEpi, false, false, true, Groups>
+                                    : (const void*)mmq_f16_kernel<BN, OutEpi, false, false, false, Groups>);
+    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k,
+                    (void*)&tiles_m, (void*)&tile_m0, (void*)&out, (void*)&g};
+    return hipLaunchKernel(f, dim3((unsigned)std::min<int64_t>(tiles, 256)), dim3(NT), args, 0, stream);
 }
 
 }  // namespace mmq

@@ -361,13 +361,13 @@ constexpr int min_waves_per_simd() {
     return L == kRepacked && N == 8 ? 4 : 1;
 }
 
-template <int N, int SW, bool H, int L>
+template <int N, int SW, class O, int L>
 __global__ __launch_bounds__(64 * kMaxWaves)
 __attribute__((amdgpu_waves_per_eu(min_waves_per_simd<N, L>()))) void mmq_gemv_kernel(const uint8_t* __restrict__ w,
                                                                   const int8_t* __restrict__ q,
                                                                   const uint32_t* __restrict__ ds,
                                                                   int M, int K,
-                                                                  void* __restrict__ out) {
+                                                                  O out) {
     __shared__ float red[kMaxWaves][N][16];
     extern __shared__ __attribute__((aligned(16))) uint8_t staged[];   // W x 2 areas (staged layout)
 
@@ -452,13 +452,13 @@ __attribute__((amdgpu_waves_per_eu(min_waves_per_simd<N, L>()))) void mmq_gemv_k
         const int t = e >> 4, rr = e & 15;
         float sum = red[0][t][rr];
         for (int v = 1; v < W; ++v) sum += red[v][t][rr];
-        if (row0 + rr < M) store_out<H>(out, (int64_t)t * M + row0 + rr, sum);
+        if (row0 + rr < M) out.put(t, row0 + rr, sum);
     }
 }
 
 template <int N, int L>
 hipError_t launch_n(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                    void* out, bool half_out, hipStream_t stream) {
+                    const Out& out, hipStream_t stream) {
     const int S = k / 256;
     const int rows = (m + 15) / 16;
     // The super-blocks of a row are split over the 4 waves of a workgroup
@@ -468,13 +468,15 @@ hipError_t launch_n(const uint8_t* w, int m, int k, const int8_t* q, const uint3
     constexpr int SW = 4;
     const size_t lds = L == kStaged ? (size_t)waves * kStagedArea
                        : L == kStagedPf ? (size_t)waves * 2 * kStagedArea : 0;
-    if (half_out)
-        hipLaunchKernelGGL((mmq_gemv_kernel<N, SW, true, L>), dim3(rows), dim3(64 * waves), lds, stream,
-                           w, q, ds, m, k, out);
+    const auto go = [&](auto o) {
+        hipLaunchKernelGGL((mmq_gemv_kernel<N, SW, decltype(o), L>), dim3(rows), dim3(64 * waves), lds, stream,
+                           w, q, ds, m, k, o);
+        return hipGetLastError();
+    };
+    if constexpr (L == kRepacked)
+        return with_out_f32(out, go);
     else
-        hipLaunchKernelGGL((mmq_gemv_kernel<N, SW, false, L>), dim3(rows), dim3(64 * waves), lds, stream,
-                           w, q, ds, m, k, out);
-    return hipGetLastError();
+        return with_out(out, go);
 }
 
 // Token counts each layout is launched for (the staged layouts up to 6
@@ -486,24 +488,23 @@ constexpr bool serves(int n) {
 }
 
 template <int L, int N>
-hipError_t launch_if(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, void* out,
-                     bool half_out, hipStream_t stream) {
-    if constexpr (serves<L>(N)) return launch_n<N, L>(w, m, k, q, ds, out, half_out, stream);
+hipError_t launch_if(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Out& out, hipStream_t stream) {
+    if constexpr (serves<L>(N)) return launch_n<N, L>(w, m, k, q, ds, out, stream);
     return hipErrorInvalidValue;
 }
 
 template <int L>
 hipError_t launch_any(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                      void* out, bool half_out, hipStream_t stream) {
+                      const Out& out, hipStream_t stream) {
     switch (n) {
-        case 1: return launch_if<L, 1>(w, m, k, q, ds, out, half_out, stream);
-        case 2: return launch_if<L, 2>(w, m, k, q, ds, out, half_out, stream);
-        case 3: return launch_if<L, 3>(w, m, k, q, ds, out, half_out, stream);
-        case 4: return launch_if<L, 4>(w, m, k, q, ds, out, half_out, stream);
-        case 5: return launch_if<L, 5>(w, m, k, q, ds, out, half_out, stream);
-        case 6: return launch_if<L, 6>(w, m, k, q, ds, out, half_out, stream);
-        case 7: return launch_if<L, 7>(w, m, k, q, ds, out, half_out, stream);
-        case 8: return launch_if<L, 8>(w, m, k, q, ds, out, half_out, stream);
+        case 1: return launch_if<L, 1>(w, m, k, q, ds, out, stream);
+        case 2: return launch_if<L, 2>(w, m, k, q, ds, out, stream);
+        case 3: return launch_if<L, 3>(w, m, k, q, ds, out, stream);
+        case 4: return launch_if<L, 4>(w, m, k, q, ds, out, stream);
+        case 5: return launch_if<L, 5>(w, m, k, q, ds, out, stream);
+        case 6: return launch_if<L, 6>(w, m, k, q, ds, out, stream);
+        case 7: return launch_if<L, 7>(w, m, k, q, ds, out, stream);
+        case 8: return launch_if<L, 8>(w, m, k, q, ds, out, stream);
         default: return hipErrorInvalidValue;
     }
 }
@@ -511,23 +512,21 @@ hipError_t launch_any(const uint8_t* w, int m, int k, const int8_t* q, const uin
 }  // namespace
 
 hipError_t launch_mmq_fp32_gemv(const uint8_t* w, int m, int k, const int8_t* q,
-                                const uint32_t* ds, int n, void* out, bool half_out,
-                                hipStream_t stream) {
+                                const uint32_t* ds, int n, const Out& out, hipStream_t stream) {
     // Staging through LDS pays while the stream, not the vector work, is the
     // bound; the next step's copy in flight pays when a wave has at least 4
     // steps (4 waves of 4-block steps: 64 super-blocks per row).  Measured
     // on the 28672 x 8192 and 8192 x 28672 matrices, 1-8 tokens.
     const bool pf = k / 256 >= 64;
     if (n <= 5 || (n == 6 && pf))
-        return pf ? launch_any<kStagedPf>(w, m, k, q, ds, n, out, half_out, stream)
-                  : launch_any<kStaged>(w, m, k, q, ds, n, out, half_out, stream);
-    return launch_any<kDirect>(w, m, k, q, ds, n, out, half_out, stream);
+        return pf ? launch_any<kStagedPf>(w, m, k, q, ds, n, out, stream)
+                  : launch_any<kStaged>(w, m, k, q, ds, n, out, stream);
+    return launch_any<kDirect>(w, m, k, q, ds, n, out, stream);
 }
 
 hipError_t launch_mmq_fp32_gemv_repacked(const uint8_t* wr, int m, int k, const int8_t* q,
-                                         const uint32_t* ds, int n, void* out, bool half_out,
-                                         hipStream_t stream) {
-    return launch_any<kRepacked>(wr, m, k, q, ds, n, out, half_out, stream);
+                                         const uint32_t* ds, int n, const Out& out, hipStream_t stream) {
+    return launch_any<kRepacked>(wr, m, k, q, ds, n, out, stream);
 }
 
 }  // namespace mmq

@@ -25,6 +25,8 @@
 //   kDots  exact int32 dots[t][o][c] (parity / inspection entry point);
 //   kFp32  float32 out[t][o] with the two-term fold applied per chunk;
 //   kF16   the same, stored as binary16 (nearest-even from the float32 value).
+#include <type_traits>
+
 #include "internal.h"
 #include "kquant_device.h"
 
@@ -184,8 +186,9 @@ __global__ __launch_bounds__(NT) void mmq_i8_kernel(const uint8_t* __restrict__ 
     }
 
     if (EPI != kDots) {
-        constexpr bool H = EPI == kF16;
-        const bool vec = (M & 3) == 0;
+        typedef typename std::conditional<EPI == kF16, OutF16, OutF32>::type O;
+        const O out{static_cast<decltype(O::p)>(outp), M};
+        const bool vec = out.vec();
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -195,14 +198,13 @@ __global__ __launch_bounds__(NT) void mmq_i8_kernel(const uint8_t* __restrict__ 
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const int o = row0 + wm * 64 + mt * 32 + 8 * jj + 4 * g;
-                    const int64_t idx = (int64_t)tok * M + o;
                     if (vec && o + 3 < M) {
-                        store_out4<H>(outp, idx, acc[mt][nt][4 * jj], acc[mt][nt][4 * jj + 1],
+                        out.put4(tok, o, acc[mt][nt][4 * jj], acc[mt][nt][4 * jj + 1],
                                       acc[mt][nt][4 * jj + 2], acc[mt][nt][4 * jj + 3]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (o + i < M) store_out<H>(outp, idx + i, acc[mt][nt][4 * jj + i]);
+                            if (o + i < M) out.put(tok, o + i, acc[mt][nt][4 * jj + i]);
                     }
                 }
             }
@@ -228,9 +230,9 @@ hipError_t launch_mmq_dots(const uint8_t* w, int m, int k, const int8_t* q, int 
 }
 
 hipError_t launch_mmq_fp32(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                           int n, void* out, bool half_out, hipStream_t stream) {
-    return half_out ? launch<kF16>(w, m, k, q, ds, n, out, stream)
-                    : launch<kFp32>(w, m, k, q, ds, n, out, stream);
+                           int n, const Out& out, hipStream_t stream) {
+    return out.kind == kOutF16 ? launch<kF16>(w, m, k, q, ds, n, out.epi.p, stream)
+                               : launch<kFp32>(w, m, k, q, ds, n, out.epi.p, stream);
 }
 
 }  // namespace mmq

@@ -35,7 +35,10 @@
 // 210 bytes into LDS with aligned 16-byte loads (two raw areas alternate,
 // the next super-block's copied during the current one), and take every
 // field from there as aligned dwords shifted into place.
+#include <algorithm>
+
 #include "f16_operand.h"
+#include "group.h"
 #include "internal.h"
 #include "kquant_device.h"
 #include "q6k_device.h"
@@ -121,12 +124,17 @@ __device__ __forceinline__ void item_of(int pt, int& row, int& gi, int& kh) {
     kh = pt >> 8;
 }
 
+// The tile's tokens are rows src.row(0 .. ) of q and ds, which hold q_rows
+// rows (a plain call passes its tile's first token's q and ds).  The weight
+// resource ends with the matrix of M rows at w, the expert's own in a grouped
+// call.
+template <bool QT, class Grp>
 __device__ __forceinline__ void init_src(Src& p, const uint8_t* __restrict__ w,
                                          const int8_t* __restrict__ q,
-                                         const uint32_t* __restrict__ ds, int pt, int row0,
-                                         int tok0, int M, int N, int K) {
+                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& src, uint32_t q_rows,
+                                         int pt, int row0, int tok0, int M, int K) {
     const int S = K >> 8, C = K >> 5;
-    const int rows = min(BM, M - row0), toks = min(BN, N - tok0);
+    const int rows = min(BM, M - row0);
     const int64_t rbytes = (int64_t)S * kQ6kBlockBytes;
     // The raw copy reads whole 16-byte pieces, up to 14 bytes past a row's
     // block: past the workgroup's last row that is the next row (16 more
@@ -136,15 +144,15 @@ __device__ __forceinline__ void init_src(Src& p, const uint8_t* __restrict__ w,
     p.rbytes = (int)rbytes;
     p.w = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(w + (int64_t)row0 * rbytes), 0,
                                             p.extent, kBufferFlags);
-    p.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(q + (int64_t)tok0 * K), 0,
-                                            (int)((uint32_t)toks * (uint32_t)K), kBufferFlags);   // up to 2^31 bytes
-    p.ds = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(ds + (int64_t)tok0 * C), 0,
-                                             toks * C * 4, kBufferFlags);
+    p.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(q), 0, (int)(q_rows * (uint32_t)K), kBufferFlags);
+    p.ds = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(ds), 0, (int)(q_rows * (uint32_t)(C * 4)),
+                                             kBufferFlags);
     // q8 piece pt: token pt & 127, 16-byte piece pt >> 7 of the stage's 64 bytes
-    p.y = min(pt & (BN - 1), toks - 1) * K + 16 * (pt >> 7);
-    p.qt = reinterpret_cast<const uint16_t*>(q) + (int64_t)(tok0 >> 7) * (K >> 7) * (kQtBlockBytes / 2);
+    const uint32_t tok = src.row(pt & (BN - 1));
+    p.y = (int)(tok * (uint32_t)K + 16 * (pt >> 7));
+    if (QT) p.qt = reinterpret_cast<const uint16_t*>(q) + (int64_t)(tok0 >> 7) * (K >> 7) * (kQtBlockBytes / 2);
     // scale word (threads < 256): token pt & 127, chunk-in-stage pt >> 7
-    p.word = (min(pt & (BN - 1), toks - 1) * C + ((pt >> 7) & 1)) * 4;
+    p.word = (int)((tok * (uint32_t)C + ((pt >> 7) & 1)) * 4);
 }
 
 // Offset in the resource of row r's block of super-block sb (rows past the
@@ -361,19 +369,15 @@ constexpr int kGroup = 256;
 // LDS stages alternate: while the consumers work on stage s, the producers
 // fill stage s+1, their loads running one stage further ahead in registers.
 // One workgroup barrier per stage.
-template <bool H, bool QT, bool BIG>
-__global__ __launch_bounds__(NT) void mmq_q6k_f16_kernel(const uint8_t* __restrict__ w,
-                                                         const int8_t* __restrict__ q,
-                                                         const uint32_t* __restrict__ ds,
-                                                         int M, int N, int K, int tiles_m,
-                                                         void* __restrict__ out) {
-    __shared__ Stage stage[2];
-    __shared__ StageB stage_b[2];
-    __shared__ Raw16 raw[2];
-
+//
+// q6k_tile is one tile: rows row0 .. row0 + 127, and the N - tok0 (at most BN)
+// tokens of src, written as tokens tok0 .. of out.
+template <class O, bool QT, bool BIG, class Grp>
+__device__ __forceinline__ void q6k_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
+                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& tokens,
+                                         uint32_t q_rows, int M, int N, int K, int row0, int tok0, const O& out,
+                                         Stage (&stage)[2], StageB (&stage_b)[2], Raw16 (&raw)[2]) {
     const int tid = threadIdx.x;
-    const int bm = blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
-    const int row0 = bm * BM, tok0 = bn * BN;
     const int stages = K >> 6;   // a multiple of 4
 
     if (tid >= CT) {
@@ -385,7 +389,7 @@ __global__ __launch_bounds__(NT) void mmq_q6k_f16_kernel(const uint8_t* __restri
         const int pt = tid - CT;
         const int rows = min(BM, M - row0);
         Src src;
-        init_src(src, w, q, ds, pt, row0, tok0, M, N, K);
+        init_src<QT>(src, w, q, ds, tokens, q_rows, pt, row0, tok0, M, K);
         const int S = K >> 8;
         Raw ra, rb;
         RawPieces rp;
@@ -452,7 +456,7 @@ __global__ __launch_bounds__(NT) void mmq_q6k_f16_kernel(const uint8_t* __restri
 #pragma unroll
         for (int a = 0; a < 2; ++a) acc[a] += acc2[a];
 
-    const bool vec = (M & 3) == 0;
+    const bool vec = out.vec();
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
         const int tok = tok0 + wn * 32 + l32;
@@ -460,45 +464,84 @@ __global__ __launch_bounds__(NT) void mmq_q6k_f16_kernel(const uint8_t* __restri
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int o = row0 + wm * 64 + rt * 32 + 8 * jj + 4 * g;
-            const int64_t idx = (int64_t)tok * M + o;
             if (vec && o + 3 < M) {
-                store_out4<H>(out, idx, acc[rt][4 * jj], acc[rt][4 * jj + 1], acc[rt][4 * jj + 2],
-                              acc[rt][4 * jj + 3]);
+                out.put4(tok, o, acc[rt][4 * jj], acc[rt][4 * jj + 1], acc[rt][4 * jj + 2],
+                         acc[rt][4 * jj + 3]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (o + i < M) store_out<H>(out, idx + i, acc[rt][4 * jj + i]);
+                    if (o + i < M) out.put(tok, o + i, acc[rt][4 * jj + i]);
             }
         }
     }
 }
 
-}  // namespace
+template <class O, bool QT, bool BIG, class Grp>
+__global__ __launch_bounds__(NT) void mmq_q6k_f16_kernel(const uint8_t* __restrict__ w,
+                                                         const int8_t* __restrict__ q,
+                                                         const uint32_t* __restrict__ ds,
+                                                         int M, int N, int K, int tiles_m,
+                                                         O out, Grp grp) {
+    __shared__ Stage stage[2];
+    __shared__ StageB stage_b[2];
+    __shared__ Raw16 raw[2];
+    if constexpr (!Grp::kOn) {
+        const int bm = blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
+        const int tok0 = bn * BN, toks = min(BN, N - tok0);
+        q6k_tile<O, QT, BIG, Grp>(w, QT ? q : q + (int64_t)tok0 * K, ds + (int64_t)tok0 * (K >> 5),
+                                  TokenRows<Grp>(grp, Item{}, toks), (uint32_t)toks, M, N, K, bm * BM, tok0, out,
+                                  stage, stage_b, raw);
+    } else {
+        // tile i: row tile i % tiles_m of item i / tiles_m
+        for (int i = blockIdx.x;; i += gridDim.x) {
+            const Item it = find_item<BN>(grp, i / tiles_m);
+            if (!it.valid) return;   // the same for every wave
+            O o = out;
+            o.advance(it.start);
+            if (o.bias) o.bias += (int64_t)it.expert * M;
+            q6k_tile<O, QT, BIG, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kQ6kBlockBytes, q, ds,
+                                      TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, it.count, K,
+                                      i % tiles_m * BM, 0, o, stage, stage_b, raw);
+        }
+    }
+}
 
-hipError_t launch_q6k_f16(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                          void* out, bool half_out, hipStream_t stream) {
+template <bool QT, class O>
+hipError_t launch(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, O out,
+                  hipStream_t stream) {
     int tiles_m = (m + BM - 1) / BM;
     const int64_t tiles = (int64_t)tiles_m * ((n + BN - 1) / BN);
+    NoGroups none;
     void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k,
-                    (void*)&tiles_m, (void*)&out};
-    const bool big = (k >> 8) > kGroup;
-    const void* f = half_out ? (big ? (const void*)mmq_q6k_f16_kernel<true, false, true>
-                                    : (const void*)mmq_q6k_f16_kernel<true, false, false>)
-                             : (big ? (const void*)mmq_q6k_f16_kernel<false, false, true>
-                                    : (const void*)mmq_q6k_f16_kernel<false, false, false>);
+                    (void*)&tiles_m, (void*)&out, (void*)&none};
+    const void* f = (k >> 8) > kGroup ? (const void*)mmq_q6k_f16_kernel<O, QT, true, NoGroups>
+                                      : (const void*)mmq_q6k_f16_kernel<O, QT, false, NoGroups>;
     return hipLaunchKernel(f, dim3((unsigned)tiles), dim3(NT), args, 0, stream);
 }
 
+}  // namespace
+
+hipError_t launch_q6k_f16(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
+                          const Out& out, hipStream_t stream) {
+    return with_out(out, [&](auto o) { return launch<false>(w, m, k, q, ds, n, o, stream); });
+}
+
 hipError_t launch_q6k_f16_tiles(const uint8_t* w, int m, int k, const uint16_t* qt, const uint32_t* ds,
-                                int n, float* out, hipStream_t stream) {
-    int tiles_m = (m + BM - 1) / BM;
-    const int64_t tiles = (int64_t)tiles_m * ((n + BN - 1) / BN);
+                                int n, const Out& out, hipStream_t stream) {
     const int8_t* q = reinterpret_cast<const int8_t*>(qt);
+    return with_out_f32(out, [&](auto o) { return launch<true>(w, m, k, q, ds, n, o, stream); });
+}
+
+hipError_t launch_q6k_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
+                                  const Groups& g, const OutEpi& out, hipStream_t stream) {
+    int tiles_m = (m + BM - 1) / BM, n = 0;
+    // a workgroup fills a CU
+    const int64_t tiles = most_items(g.experts, g.slots, g.lo, g.hi, BN) * tiles_m;
+    const void* f = (k >> 8) > kGroup ? (const void*)mmq_q6k_f16_kernel<OutEpi, false, true, Groups>
+                                      : (const void*)mmq_q6k_f16_kernel<OutEpi, false, false, Groups>;
     void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k,
-                    (void*)&tiles_m, (void*)&out};
-    const void* f = (k >> 8) > kGroup ? (const void*)mmq_q6k_f16_kernel<false, true, true>
-                                      : (const void*)mmq_q6k_f16_kernel<false, true, false>;
-    return hipLaunchKernel(f, dim3((unsigned)tiles), dim3(NT), args, 0, stream);
+                    (void*)&tiles_m, (void*)&out, (void*)&g};
+    return hipLaunchKernel(f, dim3((unsigned)std::min<int64_t>(tiles, 256)), dim3(NT), args, 0, stream);
 }
 
 }  // namespace mmq

@@ -64,12 +64,12 @@ struct SmallLds {
     };
 };
 
-template <int T, int RB, bool PF, bool H>
+template <int T, int RB, bool PF, class O>
 __global__ __launch_bounds__(NT) void mmq_small_kernel(const uint8_t* __restrict__ w,
                                                        const int8_t* __restrict__ q,
                                                        const uint32_t* __restrict__ ds,
                                                        int M, int N, int K,
-                                                       void* __restrict__ out) {
+                                                       O out) {
     __shared__ SmallLds<T, RB> L;
 
     const int lane = threadIdx.x & 63;
@@ -263,19 +263,20 @@ __global__ __launch_bounds__(NT) void mmq_small_kernel(const uint8_t* __restrict
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int tok = 16 * tt + 4 * (l >> 4) + i;
-            if (tok < N) store_out<H>(out, (int64_t)tok * M + row, sum[i]);
+            if (tok < N) out.put(tok, row, sum[i]);
         }
     }
 }
 
 template <int T, bool PF>
 hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                    void* out, bool half_out, hipStream_t stream) {
+                    const Out& out, hipStream_t stream) {
     constexpr int RB = 2;
-    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&out};
-    const void* f = half_out ? (const void*)mmq_small_kernel<T, RB, PF, true>
-                             : (const void*)mmq_small_kernel<T, RB, PF, false>;
-    return hipLaunchKernel(f, dim3((unsigned)((m + 16 * RB - 1) / (16 * RB))), dim3(NT), args, 0, stream);
+    return with_out(out, [&](auto o) {
+        void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&o};
+        return hipLaunchKernel((const void*)mmq_small_kernel<T, RB, PF, decltype(o)>,
+                               dim3((unsigned)((m + 16 * RB - 1) / (16 * RB))), dim3(NT), args, 0, stream);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -352,12 +353,12 @@ __device__ __forceinline__ void issue_copies(uint8_t* wdst, uint8_t* tdst, const
                 toff[tt * kTLoads + c] + sb * 256, 0, 0, 0);
 }
 
-template <int T, bool PF, bool H>
+template <int T, bool PF, class O>
 __global__ __launch_bounds__(kFewNT) void mmq_few_kernel(const uint8_t* __restrict__ w,
                                                        const int8_t* __restrict__ q,
                                                        const uint32_t* __restrict__ ds,
                                                        int M, int N, int K,
-                                                       void* __restrict__ out) {
+                                                       O out) {
     __shared__ FewLds<T, PF> L;
 
     const int lane = threadIdx.x & 63;
@@ -532,24 +533,25 @@ __global__ __launch_bounds__(kFewNT) void mmq_few_kernel(const uint8_t* __restri
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int tok = 16 * tt + 4 * (l >> 4) + i;
-            if (tok < N) store_out<H>(out, (int64_t)tok * M + row, sum[i]);
+            if (tok < N) out.put(tok, row, sum[i]);
         }
     }
 }
 
 template <int T, bool PF>
 hipError_t launch_few(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                    void* out, bool half_out, hipStream_t stream) {
-    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&out};
-    const void* f = half_out ? (const void*)mmq_few_kernel<T, PF, true>
-                             : (const void*)mmq_few_kernel<T, PF, false>;
-    return hipLaunchKernel(f, dim3((unsigned)((m + 15) / 16)), dim3(kFewNT), args, 0, stream);
+                    const Out& out, hipStream_t stream) {
+    return with_out(out, [&](auto o) {
+        void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&o};
+        return hipLaunchKernel((const void*)mmq_few_kernel<T, PF, decltype(o)>, dim3((unsigned)((m + 15) / 16)),
+                               dim3(kFewNT), args, 0, stream);
+    });
 }
 
 }  // namespace
 
 hipError_t launch_mmq_fp32_small(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                                 int n, void* out, bool half_out, hipStream_t stream) {
+                                 int n, const Out& out, hipStream_t stream) {
     // Prefetching the next super-block into a second register set pays when
     // each wave has many steps (8192 x 28672: 14 per wave, 16 tokens 67 ->
     // 56 us) and costs occupancy when it has few (28672 x 8192: 4 per wave,
@@ -557,14 +559,14 @@ hipError_t launch_mmq_fp32_small(const uint8_t* w, int m, int k, const int8_t* q
     if (n <= 16) {
         // the second copy area pays from 16 super-blocks per wave (8192 x
         // 28672: 28 per wave, 52 -> 50 us; 28672 x 8192: 8 per wave, 49 -> 59 us)
-        return (k / 256) / kFewWaves >= 16 ? launch_few<1, true>(w, m, k, q, ds, n, out, half_out, stream)
-                                           : launch_few<1, false>(w, m, k, q, ds, n, out, half_out, stream);
+        return (k / 256) / kFewWaves >= 16 ? launch_few<1, true>(w, m, k, q, ds, n, out, stream)
+                                           : launch_few<1, false>(w, m, k, q, ds, n, out, stream);
     }
     const bool pf = (k / 256) / WAVES >= 8;
-    if (n <= 32) return pf ? launch_t<2, true>(w, m, k, q, ds, n, out, half_out, stream)
-                           : launch_t<2, false>(w, m, k, q, ds, n, out, half_out, stream);
-    if (n <= 48) return launch_t<3, false>(w, m, k, q, ds, n, out, half_out, stream);
-    return launch_t<4, false>(w, m, k, q, ds, n, out, half_out, stream);
+    if (n <= 32) return pf ? launch_t<2, true>(w, m, k, q, ds, n, out, stream)
+                           : launch_t<2, false>(w, m, k, q, ds, n, out, stream);
+    if (n <= 48) return launch_t<3, false>(w, m, k, q, ds, n, out, stream);
+    return launch_t<4, false>(w, m, k, q, ds, n, out, stream);
 }
 
 }  // namespace mmq

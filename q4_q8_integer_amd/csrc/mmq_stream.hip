@@ -304,11 +304,11 @@ __device__ __forceinline__ void compute_step(const uint8_t* area, const uint8_t*
 // Workgroup: tiles TG = TQ * TPW (8 rows each) from tile blockIdx.x * TG;
 // W = TQ * WPT waves; wave w owns local tiles w % TQ + j TQ (j < TPW) and
 // takes the steps o, o + WPT, .. (o = w / TQ) of each phase's four.
-template <int G, bool H, int TPW>
+template <int G, class O, int TPW>
 __global__ __launch_bounds__(64 * kMaxWaves) void mmq_stream_kernel(const uint8_t* __restrict__ w,
                                                                      const int8_t* __restrict__ q,
                                                                      const uint32_t* __restrict__ ds, int M, int N,
-                                                                     int K, void* __restrict__ out, int TQ, int WPT) {
+                                                                     int K, O out, int TQ, int WPT) {
     typedef Phase<G> P;
     // Token phases (two buffers, one array each for rows and words, indexed
     // by phase parity) and two weight areas per wave, as separate arrays:
@@ -463,40 +463,41 @@ __global__ __launch_bounds__(64 * kMaxWaves) void mmq_stream_kernel(const uint8_
                 for (int ss = 0; ss < 4; ++ss) sum += rp[32 * hh + 8 * ss];
         }
         const int row = (tile0 + lt) * kRT + rr;
-        if (gv < N && row < M) store_out<H>(out, (int64_t)gv * M + row, sum);
+        if (gv < N && row < M) out.put(gv, row, sum);
     }
 }
 
 template <int G, int TPW>
-hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, void* out,
-                    bool half_out, int tq, int wpt, hipStream_t stream) {
-    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&out,
-                    (void*)&tq, (void*)&wpt};
-    const void* f = half_out ? (const void*)mmq_stream_kernel<G, true, TPW>
-                             : (const void*)mmq_stream_kernel<G, false, TPW>;
+hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
+                    const Out& out, int tq, int wpt, hipStream_t stream) {
     const int tiles = (m + kRT - 1) / kRT, tg = tq * TPW;
-    return hipLaunchKernel(f, dim3((unsigned)((tiles + tg - 1) / tg)), dim3(64 * tq * wpt), args, 0, stream);
+    return with_out(out, [&](auto o) {
+        void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&o,
+                        (void*)&tq, (void*)&wpt};
+        return hipLaunchKernel((const void*)mmq_stream_kernel<G, decltype(o), TPW>,
+                               dim3((unsigned)((tiles + tg - 1) / tg)), dim3(64 * tq * wpt), args, 0, stream);
+    });
 }
 
 template <int G>
-hipError_t launch_g(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, void* out,
-                    bool half_out, hipStream_t stream) {
+hipError_t launch_g(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
+                    const Out& out, hipStream_t stream) {
     int tq, tpw, wpt;
     stream_layout(m, tq, tpw, wpt);
     wpt = std::min(wpt, Phase<G>::kP / kSlots);   // the steps of a phase per tile
-    return tpw == 2 ? launch_t<G, 2>(w, m, k, q, ds, n, out, half_out, tq, wpt, stream)
-                    : launch_t<G, 1>(w, m, k, q, ds, n, out, half_out, tq, wpt, stream);
+    return tpw == 2 ? launch_t<G, 2>(w, m, k, q, ds, n, out, tq, wpt, stream)
+                    : launch_t<G, 1>(w, m, k, q, ds, n, out, tq, wpt, stream);
 }
 
 }  // namespace
 
 hipError_t launch_mmq_fp32_stream(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                                  void* out, bool half_out, hipStream_t stream) {
+                                  const Out& out, hipStream_t stream) {
     switch ((n + 3) / 4) {
-        case 1: return launch_g<1>(w, m, k, q, ds, n, out, half_out, stream);
-        case 2: return launch_g<2>(w, m, k, q, ds, n, out, half_out, stream);
-        case 3: return launch_g<3>(w, m, k, q, ds, n, out, half_out, stream);
-        case 4: return launch_g<4>(w, m, k, q, ds, n, out, half_out, stream);
+        case 1: return launch_g<1>(w, m, k, q, ds, n, out, stream);
+        case 2: return launch_g<2>(w, m, k, q, ds, n, out, stream);
+        case 3: return launch_g<3>(w, m, k, q, ds, n, out, stream);
+        case 4: return launch_g<4>(w, m, k, q, ds, n, out, stream);
         default: return hipErrorInvalidValue;
     }
 }

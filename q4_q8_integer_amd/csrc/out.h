@@ -1,0 +1,152 @@
+// out.h - where the float32 results of a fold kernel go: the kernels take one
+// of three output types as a template parameter and hand it each result with
+// its token and row.
+//
+//   OutF32  float32 [n][m]
+//   OutF16  binary16 [n][m], rounded to nearest-even from the float32 value
+//   OutEpi  act(v + bias[row]) + residual[token][row], float32 or binary16,
+//           rows of the output and the residual at strides of their own
+//
+// The epilogue is float32 throughout and rounds once, at a binary16 store.
+// Its choices (activation, types, which operands there are) are uniform
+// run-time values: per output they cost a few scalar branches in kernels
+// that spend k / 32 vector operations on it, where a template per choice
+// would multiply every kernel by 40.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mmq {
+
+typedef float out4f __attribute__((ext_vector_type(4)));
+typedef _Float16 out4h __attribute__((ext_vector_type(4)));
+
+struct OutF32 {
+    float* p;
+    int64_t stride;   // m
+    __device__ __forceinline__ bool vec() const { return (stride & 3) == 0; }
+    __device__ __forceinline__ void put(int64_t tok, int row, float v) const { p[tok * stride + row] = v; }
+    // Rows row .. row + 3 (row % 4 == 0, vec()).
+    __device__ __forceinline__ void put4(int64_t tok, int row, float a, float b, float c, float d) const {
+        *reinterpret_cast<float4*>(p + tok * stride + row) = make_float4(a, b, c, d);
+    }
+};
+
+struct OutF16 {
+    _Float16* p;
+    int64_t stride;   // m
+    __device__ __forceinline__ bool vec() const { return (stride & 3) == 0; }
+    __device__ __forceinline__ void put(int64_t tok, int row, float v) const { p[tok * stride + row] = (_Float16)v; }
+    __device__ __forceinline__ void put4(int64_t tok, int row, float a, float b, float c, float d) const {
+        *reinterpret_cast<out4h*>(p + tok * stride + row) =
+            out4h{(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d};
+    }
+};
+
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+// x * sigmoid(x); for x below -88 the exponential overflows and the result
+// is -0, as the exact value (below 1e-36) is to 36 digits.
+__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
+
+__device__ __forceinline__ float activate(float v, int act) {
+    switch (act) {
+        case kActRelu: return v > 0.0f ? v : 0.0f;
+        case kActSilu: return silu(v);
+        // v * Phi(v); erfc keeps its relative accuracy where 1 + erf cancels
+        case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+        // 0.5 v (1 + tanh u) = v * sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3)
+        case kActGeluTanh: {
+            const float u2 = 1.59576912160573076f * fmaf(0.044715f * v * v, v, v);
+            return v / (1.0f + expf(-u2));
+        }
+        default: return v;
+    }
+}
+
+// bias and residual may be null.  The residual may be the output itself
+// (same type and stride): a value is read by the thread that writes it.
+struct OutEpi {
+    void* p;
+    const float* bias;
+    const void* res;
+    int64_t stride, res_stride;
+    int act;
+    int half, res_half;   // binary16 output, binary16 residual
+    int vec4;             // every row of 4-value groups is aligned for put4
+
+    __device__ __forceinline__ bool vec() const { return vec4 != 0; }
+    __device__ __forceinline__ void put(int64_t tok, int row, float v) const {
+        if (bias) v += bias[row];
+        v = activate(v, act);
+        if (res) {
+            const int64_t i = tok * res_stride + row;
+            v += res_half ? (float)static_cast<const _Float16*>(res)[i] : static_cast<const float*>(res)[i];
+        }
+        if (half)
+            static_cast<_Float16*>(p)[tok * stride + row] = (_Float16)v;
+        else
+            static_cast<float*>(p)[tok * stride + row] = v;
+    }
+    __device__ __forceinline__ void put4(int64_t tok, int row, float a, float b, float c, float d) const {
+        out4f v = out4f{a, b, c, d};
+        if (bias) v += *reinterpret_cast<const out4f*>(bias + row);
+        if (act != kActNone)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = activate(v[i], act);
+        if (res) {
+            const int64_t i = tok * res_stride + row;
+            if (res_half) {
+                const out4h r = *reinterpret_cast<const out4h*>(static_cast<const _Float16*>(res) + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += (float)r[j];
+            } else {
+                v += *reinterpret_cast<const out4f*>(static_cast<const float*>(res) + i);
+            }
+        }
+        if (half)
+            *reinterpret_cast<out4h*>(static_cast<_Float16*>(p) + tok * stride + row) =
+                out4h{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+        else
+            *reinterpret_cast<out4f*>(static_cast<float*>(p) + tok * stride + row) = v;
+    }
+    // The output from token `toks` on.
+    __host__ __device__ __forceinline__ void advance(int64_t toks) {
+        p = static_cast<char*>(p) + toks * stride * (half ? 2 : 4);
+        if (res) res = static_cast<const char*>(res) + toks * res_stride * (res_half ? 2 : 4);
+    }
+};
+
+// The output of a launch: which of the three, and its values (for OutF32 and
+// OutF16 only p and stride).
+enum OutKind { kOutF32, kOutF16, kOutEpi };
+struct Out {
+    OutKind kind;
+    OutEpi epi;
+    static Out plain(void* p, int64_t m, bool half) {
+        Out o{};
+        o.kind = half ? kOutF16 : kOutF32;
+        o.epi.p = p;
+        o.epi.stride = m;
+        o.epi.half = half;
+        return o;
+    }
+};
+
+// f(output) with the launch's output type.
+template <class F>
+hipError_t with_out(const Out& o, F f) {
+    switch (o.kind) {
+        case kOutF32: return f(OutF32{static_cast<float*>(o.epi.p), o.epi.stride});
+        case kOutF16: return f(OutF16{static_cast<_Float16*>(o.epi.p), o.epi.stride});
+        default: return f(o.epi);
+    }
+}
+
+// The same for the entry points that have no plain binary16 form.
+template <class F>
+hipError_t with_out_f32(const Out& o, F f) {
+    return o.kind == kOutEpi ? f(o.epi) : f(OutF32{static_cast<float*>(o.epi.p), o.epi.stride});
+}
+
+}  // namespace mmq

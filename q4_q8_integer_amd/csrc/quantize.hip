@@ -25,31 +25,12 @@
 // block index and its lanes of one part write 256 contiguous bytes.  Tokens
 // past n (up to the tile's 128) get zero slots and no scale word.
 //
-// Numerics: x/da is the IEEE fp32 division (hipcc's default correctly
-// rounded divide; never built with fast-math), roundf rounds ties away from
-// zero, and v_cvt_f16_f32 rounds to nearest even keeping subnormals.
+// The quantization of a block itself is in q8_device.h.
 #include "internal.h"
+#include "q8_device.h"
 
 namespace mmq {
 namespace {
-
-// quad_perm controls: lane i of each quad reads lane i^1, or lane i^2.
-constexpr int kQuadXor1 = 0xB1;  // [1,0,3,2]
-constexpr int kQuadXor2 = 0x4E;  // [2,3,0,1]
-
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(
-                                                __builtin_bit_cast(int, v), kQuadXor1, 0xF, 0xF, false)));
-    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(
-                                                __builtin_bit_cast(int, v), kQuadXor2, 0xF, 0xF, false)));
-    return v;
-}
-
-__device__ __forceinline__ int quad_sum(int v) {
-    v += __builtin_amdgcn_mov_dpp(v, kQuadXor1, 0xF, 0xF, false);
-    v += __builtin_amdgcn_mov_dpp(v, kQuadXor2, 0xF, 0xF, false);
-    return v;
-}
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
@@ -122,44 +103,11 @@ __global__ __launch_bounds__(256) void q8_quantize_kernel(Src src, int64_t nbloc
         src.load(blk, part, v);
     }
 
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    amax = quad_max(amax);
-
-    uint32_t packed[2] = {0u, 0u};
-    int sum = 0;
-    uint32_t word = 0u;
-    if (amax > 0.0f) {
-        const float da = amax / 127.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float r = roundf(v[i] / da);
-            r = fminf(fmaxf(r, -127.0f), 127.0f);
-            const int qi = (int)r;
-            sum += qi;
-            packed[i >> 2] |= (uint32_t)(qi & 0xFF) << (8 * (i & 3));
-        }
-        word = (uint32_t)__builtin_bit_cast(unsigned short, (_Float16)da);
-    }
-    sum = quad_sum(sum);
-    word |= (uint32_t)(uint16_t)(int16_t)sum << 16;
+    uint32_t packed[2];
+    const uint32_t word = q8_block(v, packed);
 
     if (TILES) {
-        // slot ((cl * 2 + h) * 2 + g) * 128 + tt of block (tile, stage), part = 2 g + h
-        const int cl = c & 3, g = part >> 1, h = part & 1;
-        const int64_t stage = c >> 2, stages = C >> 2;
-        const int64_t slot = (((int64_t)(tok >> 7) * stages + stage) * 16 + (cl * 2 + h) * 2 + g) * 128 +
-                             (tok & 127);
-        uint32_t hv[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int qi = (int8_t)(uint8_t)(packed[i >> 2] >> (8 * (i & 3)));
-            hv[i] = __builtin_bit_cast(unsigned short, (_Float16)(float)qi);   // exact
-        }
-        *reinterpret_cast<uint4*>(qt + slot * 8) =
-            make_uint4(hv[0] | (hv[2] << 16), hv[1] | (hv[3] << 16), hv[4] | (hv[6] << 16),
-                       hv[5] | (hv[7] << 16));
+        *reinterpret_cast<uint4*>(qt + q8_slot(tok, c, part, C) * 8) = q8_slot_value(packed);
         if (part == 0 && !pad) ds[blk] = word;
     } else {
         *reinterpret_cast<uint2*>(q + blk * 32 + part * 8) = make_uint2(packed[0], packed[1]);

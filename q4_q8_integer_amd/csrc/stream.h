@@ -13,7 +13,7 @@ namespace mmq {
 // arithmetic, token operands held in LDS by a workgroup of many 8-row tiles
 // and weights streamed in 576-byte runs (mmq_stream.hip).
 hipError_t launch_mmq_fp32_stream(const uint8_t* w, int m, int k, const int8_t* q,
-                                  const uint32_t* ds, int n, void* out, bool half_out,
+                                  const uint32_t* ds, int n, const Out& out,
                                   hipStream_t stream);
 constexpr int kStreamMaxN = 16;
 

@@ -1,0 +1,157 @@
+"""mmq_fold_epilogue on the GPU: bit for bit the fold entry point without
+operands, and the 64-bit epilogue of its float32 result with them, over every
+format, every kernel the automatic choice takes, and every operand."""
+import numpy as np
+import pytest
+import torch
+
+import operator_refs as refs
+from gpu_helpers import note, to_dev
+from q4_q8_integer_amd import binding, synth
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = {"q4k": (binding.FORMAT_Q4K, binding.FORMAT_Q4K_REPACKED, binding.FORMAT_Q4K_TILES,
+                   binding.FORMAT_Q4K_REPACKED_TILES),
+           "q6k": (binding.FORMAT_Q6K, binding.FORMAT_Q6K_TILES)}
+
+
+def _plain(fmt, w, m, k, q, ds):
+    if fmt == binding.FORMAT_Q4K:
+        return binding.fp32(w, m, k, q, ds)
+    if fmt == binding.FORMAT_Q4K_REPACKED:
+        return binding.fp32_repacked(w, m, k, q, ds)
+    if fmt == binding.FORMAT_Q6K:
+        return binding.q6k_fp32(w, m, k, q, ds)
+    if fmt == binding.FORMAT_Q6K_TILES:
+        return binding.q6k_fp32_tiles(w, m, k, q, ds)
+    return binding.fp32_tiles(w, m, k, q, ds, repacked=fmt == binding.FORMAT_Q4K_REPACKED_TILES)
+
+
+def _setup(fmt, seed, m, k, n):
+    base = "q6k" if fmt in FORMATS["q6k"] else "q4k"
+    w = to_dev(refs.weights(base, seed, m, k).reshape(-1))
+    if fmt in (binding.FORMAT_Q4K_REPACKED, binding.FORMAT_Q4K_REPACKED_TILES):
+        w = binding.repack(w, m, k)
+    x = to_dev(synth.random_activations(seed, n, k) / np.float32(np.sqrt(k)))
+    q, ds = binding.quantize_tiled(x) if fmt in binding._TILE_FORMATS else binding.quantize(x)
+    return w, q, ds
+
+
+def _case(fmt, m, k, n, act, residual, f16, bias=True, seed=0):
+    note("epilogue fmt=%d m=%d k=%d n=%d act=%d residual=%s f16=%s" % (fmt, m, k, n, act, residual, f16))
+    w, q, ds = _setup(fmt, seed + n, m, k, n)
+    rng = np.random.default_rng([980, seed, m, n])
+    b = rng.standard_normal(m).astype(np.float32) if bias else None
+    r = None if residual is None else rng.standard_normal((n, m)).astype(residual)
+    fold = _plain(fmt, w, m, k, q, ds)
+    same = binding.fold_epilogue(fmt, w, m, k, q, ds, f16=f16)
+    out = binding.fold_epilogue(fmt, w, m, k, q, ds, None if b is None else to_dev(b), act,
+                                None if r is None else to_dev(r), f16=f16)
+    torch.cuda.synchronize()
+    assert torch.equal(same, fold.half() if f16 else fold), "without operands the call is the fold"
+    refs.check_epilogue(out.cpu().numpy(), fold.cpu().numpy(), b, act, r, f16,
+                        "fmt %d m %d k %d n %d act %d" % (fmt, m, k, n, act))
+
+
+# Token counts on both sides of every kernel border of a small matrix: narrow
+# (1-16), few-token (17-64), binary16; dot4 of q6_K (1-8); slices of 8 tokens
+# of the repacked dot4 kernel.
+@pytest.mark.parametrize("n", [1, 5, 8, 12, 17, 33, 50, 65, 130])
+@pytest.mark.parametrize("fmt", range(6))
+def test_epilogue_formats_and_kernels(fmt, n):
+    act = (fmt + n) % 5
+    m = 131 if n % 2 else 132                # odd rows: no 16-byte stores
+    _case(fmt, m, 512, n, act, [None, np.float32, np.float16][(fmt + n) % 3], (fmt * 3 + n) % 2 == 0)
+
+
+# Shapes that reach the dot4 (1 token), stream (3, 7, 12) and few-token (12 on
+# 5001 rows) kernels of q4_K.
+@pytest.mark.parametrize("m,k,n,kernel", [(14337, 4096, 1, binding.KERNEL_DOT4), (14337, 4096, 3, binding.KERNEL_STREAM),
+                                          (14337, 4096, 7, binding.KERNEL_STREAM), (20000, 5120, 2, binding.KERNEL_NARROW),
+                                          (5001, 256, 12, binding.KERNEL_FEW), (16384, 1024, 6, binding.KERNEL_NARROW)])
+def test_epilogue_tall_matrices(m, k, n, kernel):
+    assert binding.mmq_kernel_choice(binding.FORMAT_Q4K, m, k, n) == kernel
+    _case(binding.FORMAT_Q4K, m, k, n, binding.ACT_SILU, np.float32, False, seed=3)
+
+
+@pytest.mark.parametrize("act", range(5))
+@pytest.mark.parametrize("f16", [False, True])
+def test_activations_over_their_range(act, f16):
+    """A bias from -130 to 130 over a small fold: both tails, and zero."""
+    m, k, n = 1024, 256, 3
+    w, q, ds = _setup(binding.FORMAT_Q4K, 5, m, k, n)
+    fold = binding.fp32(w, m, k, q, ds)
+    b = np.linspace(-130, 130, m).astype(np.float32)
+    b[::97] = 0
+    if act == binding.ACT_GELU:
+        # beyond |v| = 13.5 the exact value leaves float32's normal range
+        b = (b / 10).astype(np.float32)
+    out = binding.fold_epilogue(binding.FORMAT_Q4K, w, m, k, q, ds, to_dev(b), act, f16=f16)
+    torch.cuda.synchronize()
+    refs.check_epilogue(out.cpu().numpy(), fold.cpu().numpy(), b, act, None, f16, "act %d" % act)
+
+
+def test_lowest_bias_and_far_tails_are_finite():
+    """Biases at the type's lowest and highest values (a masked output): no
+    NaN, and the tails are 0 or the value itself."""
+    m, k, n = 64, 256, 2
+    w, q, ds = _setup(binding.FORMAT_Q4K, 6, m, k, n)
+    low = torch.finfo(torch.float32).min
+    b = torch.full((m,), low, device="cuda:0")
+    b[m // 2:] = -low
+    for act in range(1, 5):
+        out = binding.fold_epilogue(binding.FORMAT_Q4K, w, m, k, q, ds, b, act).cpu()
+        assert not out.isnan().any() and (out[:, :m // 2] == 0).all() and (out[:, m // 2:] > 1e38).all(), act
+
+
+@pytest.mark.parametrize("fmt,n", [(binding.FORMAT_Q4K, 3), (binding.FORMAT_Q4K, 40), (binding.FORMAT_Q4K, 150),
+                                   (binding.FORMAT_Q4K_REPACKED, 11), (binding.FORMAT_Q6K, 4),
+                                   (binding.FORMAT_Q6K, 150)])
+@pytest.mark.parametrize("m,pad", [(96, 32), (97, 30), (96, 2)])
+def test_strided_outputs_in_place_residual(fmt, n, m, pad):
+    """Output rows as a slice of a wider array that is its own residual; the
+    columns beside it are left as they were."""
+    k = 512
+    w, q, ds = _setup(fmt, 7, m, k, n)
+    fold = _plain(fmt, w, m, k, q, ds).cpu().numpy()
+    rng = np.random.default_rng(9)
+    r = rng.standard_normal((n, m)).astype(np.float32)
+    wide = torch.full((n, m + pad), 5.0, device="cuda:0")
+    out = wide[:, :m]
+    out.copy_(to_dev(r))
+    note("epilogue strided fmt=%d n=%d m=%d pad=%d" % (fmt, n, m, pad))
+    got = binding.fold_epilogue(fmt, w, m, k, q, ds, residual=out, out=out)
+    torch.cuda.synchronize()
+    assert got is out and (wide[:, m:] == 5).all()
+    refs.check_epilogue(out.cpu().numpy(), fold, None, 0, r, False, "in place")
+
+
+def test_epilogue_row_split_launch():
+    """A prefill shape that the binary16 kernel cuts into a 128-token and a
+    64-token part: both parts read their rows of bias and residual."""
+    _case(binding.FORMAT_Q4K, 11008, 256, 512, binding.ACT_RELU, np.float32, False)
+
+
+def test_epilogue_binding_refusals():
+    m, k, n = 32, 256, 4
+    w, q, ds = _setup(binding.FORMAT_Q4K, 1, m, k, n)
+    call = lambda **kw: binding.fold_epilogue(binding.FORMAT_Q4K, w, m, k, q, ds, **kw)  # noqa: E731
+    with pytest.raises(ValueError):
+        call(bias=torch.zeros(m + 1, device="cuda:0"))
+    with pytest.raises(TypeError):
+        call(bias=torch.zeros(m, device="cuda:0", dtype=torch.float16))
+    with pytest.raises(ValueError):
+        call(residual=torch.zeros(n, m + 1, device="cuda:0"))
+    with pytest.raises(ValueError):
+        call(residual=torch.zeros(m, n, device="cuda:0").t())
+    with pytest.raises(ValueError):
+        call(residual=torch.zeros(1, m, device="cuda:0").expand(n, m))
+    with pytest.raises(TypeError):
+        call(out=torch.zeros(n, m, device="cuda:0"), f16=True)
+    with pytest.raises(binding.MMQError):
+        call(activation=9)
+    with pytest.raises(ValueError):
+        binding.fold_epilogue(binding.FORMAT_Q6K, w, m, k, q, ds)
+    with pytest.raises(TypeError):
+        binding.fold_epilogue(binding.FORMAT_Q4K_TILES, w, m, k, q, ds)
