@@ -539,9 +539,23 @@ def fp32_repacked(wr: torch.Tensor, m: int, k: int, q: torch.Tensor, ds: torch.T
 
 
 # ------------------------------------------------- epilogue, experts, norm
-def _on(dev):
-    """Make dev the current device for a call (its stream and its kernels)."""
-    return torch.cuda.device(dev)
+def _run(fn: str, dev, *args):
+    """Call the library with the current stream of dev, dev being the current
+    device meanwhile (a launch goes to the current one)."""
+    call, i = getattr(load_library(), fn), dev.index
+    if i == torch.cuda.current_device():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc != 0:
+        _check(fn, rc)
+
+
+def _on_one(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device, got %s and %s" % (dev, t.device))
 
 
 def _rows(t, dtypes, n: int, k: int, name: str) -> int:
@@ -602,7 +616,7 @@ def _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h):
         _need(h, torch.float32, "h")
         if tuple(h.shape) != (n, k):
             raise ValueError("h must be [%d, %d], got %s" % (n, k, tuple(h.shape)))
-    _same_device(x, weight, y, y_weight, gate, r, h)
+    _on_one(x.device, weight, y, y_weight, gate, r, h)
     a.x, a.y, a.y_weight, a.gate = _addr(x), _addr(y), _addr(y_weight), _addr(gate)
     a.weight, a.h, a.residual_scale, a.eps = _addr(weight), _addr(h), residual_scale, eps
     return a, n, k, r
@@ -617,8 +631,7 @@ def quantize_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, y=No
     a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
     q = torch.empty((n, k), dtype=torch.int8, device=x.device)
     ds = torch.empty((n, k // 32), dtype=torch.int32, device=x.device)
-    with _on(x.device):
-        _check("q8_quantize_norm", load_library().q8_quantize_norm(a, n, k, q.data_ptr(), ds.data_ptr(), _stream()))
+    _run("q8_quantize_norm", x.device, a, n, k, q.data_ptr(), ds.data_ptr())
     return q, ds, r
 
 
@@ -629,9 +642,7 @@ def quantize_norm_tiled(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5
     a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
     qt = torch.empty(tiles_elems(n, k), dtype=torch.int16, device=x.device)
     ds = torch.empty((n, k // 32), dtype=torch.int32, device=x.device)
-    with _on(x.device):
-        _check("q8_quantize_norm_tiled", load_library().q8_quantize_norm_tiled(
-            a, n, k, qt.data_ptr(), ds.data_ptr(), _stream()))
+    _run("q8_quantize_norm_tiled", x.device, a, n, k, qt.data_ptr(), ds.data_ptr())
     return qt, ds, r
 
 
@@ -642,8 +653,7 @@ def norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, y=None, y_wei
     if h is None:
         h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
     a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
-    with _on(x.device):
-        _check("residual_norm", load_library().residual_norm(a, n, k, _stream()))
+    _run("residual_norm", x.device, a, n, k)
     return h, r
 
 
@@ -689,10 +699,8 @@ def fold_epilogue(fmt: int, w: torch.Tensor, m: int, k: int, q: torch.Tensor, ds
         n = _tokens(q, k)
     _scale_words(ds, n, k)
     a, out = _epilogue(bias, (m,), activation, residual, n, m, out, f16, q.device)
-    _same_device(w, q, ds, bias, residual, out)
-    with _on(q.device):
-        _check("mmq_fold_epilogue", load_library().mmq_fold_epilogue(
-            fmt, w.data_ptr(), m, k, q.data_ptr(), ds.data_ptr(), n, a, out.data_ptr(), _stream()))
+    _on_one(q.device, w, ds, bias, residual, out)
+    _run("mmq_fold_epilogue", q.device, fmt, w.data_ptr(), m, k, q.data_ptr(), ds.data_ptr(), n, a, out.data_ptr())
     return out
 
 
@@ -726,11 +734,9 @@ def fold_grouped(fmt: int, w: torch.Tensor, experts: int, m: int, k: int, q: tor
     if out is not None and out.dim() == 2 and out.shape[0] < slots:
         slots = out.shape[0]
     a, out = _epilogue(bias, (experts, m), activation, residual, slots, m, out, f16, q.device)
-    _same_device(w, q, ds, offsets, rows, bias, residual, out)
-    with _on(q.device):
-        _check("mmq_fold_grouped", load_library().mmq_fold_grouped(
-            fmt, w.data_ptr(), experts, m, k, q.data_ptr(), ds.data_ptr(), tokens, _addr(rows), offsets.data_ptr(),
-            slots, a, out.data_ptr(), _stream()))
+    _on_one(q.device, w, ds, offsets, rows, bias, residual, out)
+    _run("mmq_fold_grouped", q.device, fmt, w.data_ptr(), experts, m, k, q.data_ptr(), ds.data_ptr(), tokens, _addr(rows), offsets.data_ptr(),
+            slots, a, out.data_ptr())
     return out
 
 
@@ -750,10 +756,8 @@ def route(logits: torch.Tensor, top: int, normalize: bool = True, scale: float =
     slot = torch.empty((n, top), dtype=torch.int32, device=dev)
     rows = torch.empty(n * top, dtype=torch.int32, device=dev)
     offsets = (torch.empty if n else torch.zeros)(experts + 1, dtype=torch.int32, device=dev)
-    with _on(dev):
-        _check("moe_route", load_library().moe_route(
-            logits.data_ptr(), n, experts, stride, top, normalize, scale, ids.data_ptr(), weights.data_ptr(),
-            slot.data_ptr(), rows.data_ptr(), offsets.data_ptr(), _stream()))
+    _run("moe_route", dev, logits.data_ptr(), n, experts, stride, top, normalize, scale, ids.data_ptr(), weights.data_ptr(),
+            slot.data_ptr(), rows.data_ptr(), offsets.data_ptr())
     return Routing(ids, weights, slot, rows, offsets)
 
 
@@ -775,9 +779,7 @@ def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, residual
         if tuple(residual.shape) != (n, m):
             raise ValueError("residual must be [%d, %d], got %s" % (n, m, tuple(residual.shape)))
     out = _out_tensor(out, n, m, torch.float32, y.device)
-    _same_device(y, slot, weights, residual, out)
-    with _on(y.device):
-        _check("moe_combine", load_library().moe_combine(
-            y.data_ptr(), y.dtype == torch.float16, slots, m, slot.data_ptr(), weights.data_ptr(), n, top,
-            _addr(residual), out.data_ptr(), _stream()))
+    _on_one(y.device, slot, weights, residual, out)
+    _run("moe_combine", y.device, y.data_ptr(), y.dtype == torch.float16, slots, m, slot.data_ptr(), weights.data_ptr(), n, top,
+            _addr(residual), out.data_ptr())
     return out

@@ -68,6 +68,13 @@ __device__ __forceinline__ Item find_item(const Groups& g, int i) {
     return Item{0, 0, 0, false};
 }
 
+// x, as a value the compiler knows nothing of: addresses computed from it in
+// a loop over items are not kept in registers from one item to the next.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // The most items a launch can have.
 inline int64_t most_items(int64_t experts, int64_t slots, int64_t lo, int64_t hi, int64_t tb) {
     const int64_t full = slots / lo < experts ? slots / lo : experts;   // experts with lo slots or more

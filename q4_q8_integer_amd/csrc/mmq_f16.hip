@@ -446,24 +446,22 @@ constexpr int kGroup = 256;
 // stage further ahead in registers, two with int8 codes).  One workgroup
 // barrier per stage.
 //
-// f16_tile is one tile: rows row0 .. row0 + 127, and the N - tok0 (at most TB)
-// tokens of src, written as tokens tok0 .. of out.
-template <int TB, class O, bool REP, bool QT, bool BIG, class Grp>
-__device__ __forceinline__ void f16_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
-                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& tokens,
-                                         uint32_t q_rows, int M, int N, int K, int row0, int tok0, const O& out,
-                                         Stage (&stage)[2], StageB (&stage_b)[2]) {
-    const int tid = threadIdx.x;
+// f16_produce and f16_consume are the two roles' parts of one tile: rows row0
+// .. row0 + 127, and the N - tok0 (at most TB) tokens of `tokens`, written as
+// tokens tok0 .. of out.
+template <int TB, bool REP, bool QT, class Grp>
+__device__ __forceinline__ void f16_produce(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
+                                            const uint32_t* __restrict__ ds, const TokenRows<Grp>& tokens,
+                                            uint32_t q_rows, int M, int K, int row0, int tok0, Stage (&stage)[2],
+                                            StageB (&stage_b)[2]) {
     const int stages = K >> 7;
-
-    if (tid >= CT) {
-        // ------------------------------------------------------- producer
+    {
         // Raw register sets rotate, so that the loads of later stages stay
         // in flight while stage s is converted (a register copy would force a
         // wait on them).  k is a multiple of 256, so the stage count is even.
         // Every load is unconditional (prefetches past the end re-read the
         // final stage), which lets the compiler wait only for the oldest set.
-        const int pt = tid - CT;
+        const int pt = threadIdx.x - CT;
         Src src;
         init_src<TB, REP, QT>(src, w, q, ds, tokens, q_rows, pt, row0, tok0, M, K);
         Raw ra, rb;
@@ -523,10 +521,13 @@ __device__ __forceinline__ void f16_tile(const uint8_t* __restrict__ w, const in
             }
         }
         __syncthreads();  // the consumers' last stage
-        return;
     }
+}
 
-    // ----------------------------------------------------------- consumer
+template <int TB, class O, bool BIG>
+__device__ __forceinline__ void f16_consume(int tid, int M, int N, int K, int row0, int tok0, const O& out,
+                                            const Stage (&stage)[2], const StageB (&stage_b)[2]) {
+    const int stages = K >> 7;
     const int lane = tid & 63, wave = tid >> 6;
     constexpr int RT = TB / 64;                 // 32-row tiles per wave
     constexpr int RW = 128 / (32 * RT);         // waves along the rows
@@ -595,25 +596,38 @@ __global__ __launch_bounds__(NT) void mmq_f16_kernel(const uint8_t* __restrict__
                                                      O out, Grp grp) {
     __shared__ Stage stage[2];
     __shared__ StageB stage_b[2];
+    const bool producer = threadIdx.x >= CT;
     if constexpr (!Grp::kOn) {
         // row tiles tile_m0 .. tile_m0 + tiles_m - 1 of the M rows (a launch may
         // cover part of them), token tiles of TB
         const int bm = tile_m0 + blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
         const int tok0 = bn * TB, toks = min(TB, N - tok0);
-        f16_tile<TB, O, REP, QT, BIG, Grp>(w, QT ? q : q + (int64_t)tok0 * K, ds + (int64_t)tok0 * (K >> 5),
-                                           TokenRows<Grp>(grp, Item{}, toks), (uint32_t)toks, M, N, K, bm * BM, tok0,
-                                           out, stage, stage_b);
-    } else {
-        // tile i: row tile i % tiles_m of item i / tiles_m
+        if (producer)
+            f16_produce<TB, REP, QT, Grp>(w, QT ? q : q + (int64_t)tok0 * K, ds + (int64_t)tok0 * (K >> 5),
+                                          TokenRows<Grp>(grp, Item{}, toks), (uint32_t)toks, M, K, bm * BM, tok0,
+                                          stage, stage_b);
+        else
+            f16_consume<TB, O, BIG>(threadIdx.x, M, N, K, bm * BM, tok0, out, stage, stage_b);
+    } else if (producer) {
+        // tile i: row tile i % tiles_m of item i / tiles_m.  Each role has its
+        // own loop (one loop around both keeps both roles' addresses in
+        // registers, which spills); they find the same items and meet at the
+        // same barriers.
         for (int i = blockIdx.x;; i += gridDim.x) {
             const Item it = find_item<TB>(grp, i / tiles_m);
-            if (!it.valid) return;   // the same for every wave
+            if (!it.valid) return;
+            f16_produce<TB, REP, QT, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kBlockBytes, q, ds,
+                                          TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, K, i % tiles_m * BM, 0,
+                                          stage, stage_b);
+        }
+    } else {
+        for (int i = blockIdx.x;; i += gridDim.x) {
+            const Item it = find_item<TB>(grp, i / tiles_m);
+            if (!it.valid) return;
             O o = out;
             o.advance(it.start);
             if (o.bias) o.bias += (int64_t)it.expert * M;
-            f16_tile<TB, O, REP, QT, BIG, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kBlockBytes, q, ds,
-                                               TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, it.count, K,
-                                               i % tiles_m * BM, 0, o, stage, stage_b);
+            f16_consume<TB, O, BIG>(opaque(threadIdx.x), M, it.count, K, i % tiles_m * BM, 0, o, stage, stage_b);
         }
     }
 }

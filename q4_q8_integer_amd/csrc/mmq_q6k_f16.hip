@@ -370,23 +370,22 @@ constexpr int kGroup = 256;
 // fill stage s+1, their loads running one stage further ahead in registers.
 // One workgroup barrier per stage.
 //
-// q6k_tile is one tile: rows row0 .. row0 + 127, and the N - tok0 (at most BN)
-// tokens of src, written as tokens tok0 .. of out.
-template <class O, bool QT, bool BIG, class Grp>
-__device__ __forceinline__ void q6k_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
-                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& tokens,
-                                         uint32_t q_rows, int M, int N, int K, int row0, int tok0, const O& out,
-                                         Stage (&stage)[2], StageB (&stage_b)[2], Raw16 (&raw)[2]) {
-    const int tid = threadIdx.x;
+// q6k_produce and q6k_consume are the two roles' parts of one tile: rows row0
+// .. row0 + 127, and the N - tok0 (at most BN) tokens of `tokens`, written as
+// tokens tok0 .. of out.
+template <bool QT, class Grp>
+__device__ __forceinline__ void q6k_produce(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
+                                            const uint32_t* __restrict__ ds, const TokenRows<Grp>& tokens,
+                                            uint32_t q_rows, int M, int K, int row0, int tok0, Stage (&stage)[2],
+                                            StageB (&stage_b)[2], Raw16 (&raw)[2]) {
     const int stages = K >> 6;   // a multiple of 4
-
-    if (tid >= CT) {
+    {
         // Producers.  Two register sets of q8 data alternate (stage s+1's
         // loads stay in flight while stage s is converted), and the raw copy
         // of super-block sb+1 is loaded during sb and stored after its second
         // stage: the stage barriers that follow order it before its first
         // reader and after the last reader of the area it replaces.
-        const int pt = tid - CT;
+        const int pt = threadIdx.x - CT;
         const int rows = min(BM, M - row0);
         Src src;
         init_src<QT>(src, w, q, ds, tokens, q_rows, pt, row0, tok0, M, K);
@@ -419,9 +418,13 @@ __device__ __forceinline__ void q6k_tile(const uint8_t* __restrict__ w, const in
             __syncthreads();
         }
         __syncthreads();  // the consumers' last stage
-        return;
     }
+}
 
+template <class O, bool BIG>
+__device__ __forceinline__ void q6k_consume(int tid, int M, int N, int K, int row0, int tok0, const O& out,
+                                            const Stage (&stage)[2], const StageB (&stage_b)[2]) {
+    const int stages = K >> 6;
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave & 1, wn = wave >> 1;
     const int g = lane >> 5, l32 = lane & 31;
@@ -485,23 +488,34 @@ __global__ __launch_bounds__(NT) void mmq_q6k_f16_kernel(const uint8_t* __restri
     __shared__ Stage stage[2];
     __shared__ StageB stage_b[2];
     __shared__ Raw16 raw[2];
+    const bool producer = threadIdx.x >= CT;
     if constexpr (!Grp::kOn) {
         const int bm = blockIdx.x % tiles_m, bn = blockIdx.x / tiles_m;
         const int tok0 = bn * BN, toks = min(BN, N - tok0);
-        q6k_tile<O, QT, BIG, Grp>(w, QT ? q : q + (int64_t)tok0 * K, ds + (int64_t)tok0 * (K >> 5),
-                                  TokenRows<Grp>(grp, Item{}, toks), (uint32_t)toks, M, N, K, bm * BM, tok0, out,
-                                  stage, stage_b, raw);
-    } else {
-        // tile i: row tile i % tiles_m of item i / tiles_m
+        if (producer)
+            q6k_produce<QT, Grp>(w, QT ? q : q + (int64_t)tok0 * K, ds + (int64_t)tok0 * (K >> 5),
+                                 TokenRows<Grp>(grp, Item{}, toks), (uint32_t)toks, M, K, bm * BM, tok0, stage,
+                                 stage_b, raw);
+        else
+            q6k_consume<O, BIG>(threadIdx.x, M, N, K, bm * BM, tok0, out, stage, stage_b);
+    } else if (producer) {
+        // tile i: row tile i % tiles_m of item i / tiles_m; a loop per role, as
+        // in the q4_K kernel
         for (int i = blockIdx.x;; i += gridDim.x) {
             const Item it = find_item<BN>(grp, i / tiles_m);
-            if (!it.valid) return;   // the same for every wave
+            if (!it.valid) return;
+            q6k_produce<QT, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kQ6kBlockBytes, q, ds,
+                                 TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, K, i % tiles_m * BM, 0, stage,
+                                 stage_b, raw);
+        }
+    } else {
+        for (int i = blockIdx.x;; i += gridDim.x) {
+            const Item it = find_item<BN>(grp, i / tiles_m);
+            if (!it.valid) return;
             O o = out;
             o.advance(it.start);
             if (o.bias) o.bias += (int64_t)it.expert * M;
-            q6k_tile<O, QT, BIG, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kQ6kBlockBytes, q, ds,
-                                      TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, it.count, K,
-                                      i % tiles_m * BM, 0, o, stage, stage_b, raw);
+            q6k_consume<O, BIG>(opaque(threadIdx.x), M, it.count, K, i % tiles_m * BM, 0, o, stage, stage_b);
         }
     }
 }

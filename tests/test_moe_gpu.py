@@ -211,3 +211,27 @@ def test_experts_block_in_a_graph():
         for key in ("r", "gate", "down", "out"):
             assert torch.equal(o[key], e[key]), key
         blk.check(o)
+
+
+def test_route_more_ids_than_registers_hold():
+    """70000 x 1 and 9000 x 8 ids: over 65536, where the sort reads its ids
+    twice; checked against numpy's stable sort."""
+    for n, experts, top in ((70001, 3, 1), (9001, 40, 8)):
+        rng = np.random.default_rng([996, n])
+        logits = rng.standard_normal((n, experts)).astype(np.float32)
+        logits[rng.random(n) < 0.1] = -np.inf
+        note("route n=%d experts=%d top=%d" % (n, experts, top))
+        r = binding.route(to_dev(logits), top)
+        torch.cuda.synchronize()
+        order = np.argsort(-logits, axis=1, kind="stable")[:, :top].astype(np.int32)
+        ids = np.where(np.take_along_axis(logits, order, 1) > -np.inf, order, -1)
+        assert np.array_equal(r.ids.cpu().numpy(), ids)
+        flat = ids.reshape(-1)
+        by = np.argsort(np.where(flat < 0, experts, flat), kind="stable")
+        used = int((flat >= 0).sum())
+        slot = np.full(flat.size, -1, np.int32)
+        slot[by[:used]] = np.arange(used)
+        assert np.array_equal(r.slot.cpu().numpy().reshape(-1), slot)
+        rows = r.rows.cpu().numpy()
+        assert np.array_equal(rows[:used], by[:used] // top) and (rows[used:] == -1).all()
+        assert np.array_equal(r.offsets.cpu().numpy(), np.searchsorted(np.sort(flat[flat >= 0]), np.arange(experts + 1)))
