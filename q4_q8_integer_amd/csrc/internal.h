@@ -153,6 +153,12 @@ hipError_t launch_q6k_gemv(const uint8_t* w, int m, int k, const int8_t* q, cons
                            int n, const Out& out, hipStream_t stream);
 constexpr int kQ6kGemvMaxN = 8;
 
+// out[t][o] with an epilogue for n <= kQ6kFewMaxN: int8 MFMA on 16-row tiles,
+// the waves of a workgroup split over k (mmq_q6k_few.hip).
+hipError_t launch_q6k_few(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
+                          const OutEpi& out, hipStream_t stream);
+constexpr int kQ6kFewMaxN = 64;
+
 // The matmuls grouped by expert (group.h): the kernels above over the items
 // of the experts with g.lo .. g.hi slots.  tokens_per_item: the most slots
 // one item should hold, rounded up to what the kernel has.
@@ -163,6 +169,8 @@ hipError_t launch_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, c
                               const OutEpi& out, int tokens_per_item, hipStream_t stream);
 hipError_t launch_q6k_gemv_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                                    const Groups& g, const OutEpi& out, int tokens_per_item, hipStream_t stream);
+hipError_t launch_q6k_few_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
+                                  const Groups& g, const OutEpi& out, hipStream_t stream);
 hipError_t launch_q6k_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                                   const Groups& g, const OutEpi& out, hipStream_t stream);
 

@@ -244,6 +244,13 @@ int q6k_fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const u
     if (rc != MMQ_OK || empty) return rc;
     if (!ds) return MMQ_ERR_NULL;
     if (!aligned16(ds)) return MMQ_ERR_ALIGN;
+    if (out.kind == mmq::kOutEpi && n > mmq::kQ6kGemvMaxN && n <= mmq::kQ6kFewMaxN) {
+        if (!threads_ok((m + 15) / 16, 512)) return MMQ_ERR_OVERFLOW;
+        rc = check_device();
+        if (rc != MMQ_OK) return rc;
+        return hip_status(mmq::launch_q6k_few(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out.epi,
+                                              stream));
+    }
     FoldLaunch launch = nullptr;
     rc = q6k_fold_launcher(kernel, m, n, &launch);
     if (rc != MMQ_OK) return rc;
@@ -333,9 +340,9 @@ int make_epilogue(const mmq_epilogue* e, void* out, int64_t m, int64_t rows, int
 }
 
 // -------------------------------------------------------------- grouped
-// The experts with up to kFewSlots slots run on the few-token kernels, those
-// with more on the binary16-MFMA kernels; which are which only the device
-// knows, so both are launched unless the slots cannot reach the border.
+// Experts run on the kernels that suit their slot counts, which only the
+// device knows: each kernel is launched over the experts within its range,
+// unless there are too few slots for any.
 int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t k, const int8_t* q,
                   const uint32_t* ds, int64_t tokens, const int32_t* rows, const int32_t* offsets, int64_t slots,
                   const mmq_epilogue* epilogue, void* out, hipStream_t stream) {
@@ -357,22 +364,35 @@ int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t
         !aligned16(out))
         return MMQ_ERR_ALIGN;
     if (experts > 1 && (m * (k / 256) * block) % 16 != 0) return MMQ_ERR_ALIGN;   // every expert's first row
-    const int64_t few = q6k ? mmq::kQ6kGemvMaxN : mmq::kNarrowMaxN;
     // tiles are numbered in 32 bits; one slot per item and 16 rows per tile is the most there can be
     if (mmq::most_items(experts, slots, 1, slots, 1) * ((m + 15) / 16) > kMaxDim) return MMQ_ERR_OVERFLOW;
     rc = check_device();
     if (rc != MMQ_OK) return rc;
-    mmq::Groups g{offsets, rows, (int)experts, (int)slots, (int)tokens, 1, (int)few};
-    const int64_t mean = slots / experts;
     const uint8_t* wb = static_cast<const uint8_t*>(w);
+    const int64_t mean = slots / experts;
+    mmq::Groups g{offsets, rows, (int)experts, (int)slots, (int)tokens, 0, 0};
+    // The launches, each over the experts with up to `most` slots that the one
+    // before has not taken, until there can be none left.
+    const auto take = [&](int64_t most) {
+        g.lo = g.hi + 1;
+        g.hi = (int)most;
+        return g.lo <= slots;
+    };
     const int per = slots <= 4 || mean < 1 ? 4 : mean < 4 ? 8 : 16;
-    rc = hip_status(q6k ? mmq::launch_q6k_gemv_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream)
-                        : mmq::launch_narrow_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream));
-    if (rc != MMQ_OK || slots <= few) return rc;
-    g.lo = (int)few + 1;
-    g.hi = (int)slots;
-    return hip_status(q6k ? mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream)
-                          : mmq::launch_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, mean < 96 ? 64 : 128, stream));
+    if (q6k) {
+        if ((slots <= mmq::kQ6kGemvMaxN || mean < 4) && take(mmq::kQ6kGemvMaxN))
+            rc = hip_status(mmq::launch_q6k_gemv_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream));
+        if (rc == MMQ_OK && take(mmq::kQ6kFewMaxN))
+            rc = hip_status(mmq::launch_q6k_few_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
+        if (rc == MMQ_OK && take(slots))
+            rc = hip_status(mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
+    } else {
+        if (take(mmq::kNarrowMaxN))
+            rc = hip_status(mmq::launch_narrow_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream));
+        if (rc == MMQ_OK && take(slots))
+            rc = hip_status(mmq::launch_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, mean < 96 ? 64 : 128, stream));
+    }
+    return rc;
 }
 
 // ----------------------------------------------------------------- norm

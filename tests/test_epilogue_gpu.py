@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import operator_refs as refs
-from gpu_helpers import note, to_dev
+from gpu_helpers import check_fp32, host_ds, note, to_dev
 from q4_q8_integer_amd import binding, synth
 
 pytestmark = pytest.mark.gpu
@@ -49,6 +49,12 @@ def _case(fmt, m, k, n, act, residual, f16, bias=True, seed=0):
     out = binding.fold_epilogue(fmt, w, m, k, q, ds, None if b is None else to_dev(b), act,
                                 None if r is None else to_dev(r), f16=f16)
     torch.cuda.synchronize()
+    if fmt == binding.FORMAT_Q6K and 9 <= n <= 64:
+        # a kernel of its own: its fold is held to the oracle, and the epilogue to its fold
+        fold = binding.fold_epilogue(fmt, w, m, k, q, ds)
+        torch.cuda.synchronize()
+        check_fp32(fold.cpu().numpy(), refs.fold64("q6k", w.cpu().numpy().reshape(m, -1), m, k, q.cpu().numpy(),
+                                                   host_ds(ds)), "q6k few")
     assert torch.equal(same, fold.half() if f16 else fold), "without operands the call is the fold"
     refs.check_epilogue(out.cpu().numpy(), fold.cpu().numpy(), b, act, r, f16,
                         "fmt %d m %d k %d n %d act %d" % (fmt, m, k, n, act))
@@ -63,6 +69,20 @@ def test_epilogue_formats_and_kernels(fmt, n):
     act = (fmt + n) % 5
     m = 131 if n % 2 else 132                # odd rows: no 16-byte stores
     _case(fmt, m, 512, n, act, [None, np.float32, np.float16][(fmt + n) % 3], (fmt * 3 + n) % 2 == 0)
+
+
+@pytest.mark.parametrize("n", [9, 16, 17, 31, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("m,k", [(1, 256), (37, 2048), (130, 2304), (48, 16640)])
+def test_q6k_few_tokens(m, k, n):
+    """Every token-tile count of the q6_K few-token kernel: row tiles that end
+    inside 16 rows and inside a 16-byte piece, one super-block (seven idle
+    waves), a whole round of the waves, one more, and 65."""
+    _case(binding.FORMAT_Q6K, m, k, n, n % 5, np.float32, n % 2 == 0, seed=11)
+
+
+def test_q6k_few_tokens_long_rows():
+    """Beyond 32 super-blocks per wave, where the sums move on."""
+    _case(binding.FORMAT_Q6K, 20, 256 * 600, 20, 0, None, False, bias=False, seed=12)
 
 
 # Shapes that reach the dot4 (1 token), stream (3, 7, 12) and few-token (12 on
