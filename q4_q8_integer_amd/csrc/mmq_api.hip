@@ -387,8 +387,7 @@ int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t
         if (rc == MMQ_OK && take(slots))
             rc = hip_status(mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
     } else {
-        if (take(mmq::kNarrowMaxN))
-            rc = hip_status(mmq::launch_narrow_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream));
+        if (take(mmq::kGroupFewMaxN)) rc = hip_status(mmq::launch_few_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
         if (rc == MMQ_OK && take(slots))
             rc = hip_status(mmq::launch_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, mean < 96 ? 64 : 128, stream));
     }

@@ -404,7 +404,7 @@ hipError_t launch_grouped_g(const uint8_t* w, int m, int k, const int8_t* q, con
     const int w32 = narrow_waves32(items * ((m + 31) / 32 * 32), k);
     if (w32 == 4) return launch_grouped_t<G, 32, 4>(w, m, k, q, ds, g, out, 4, stream);
     if (w32 == 8) return launch_grouped_t<G, 32, 8>(w, m, k, q, ds, g, out, 8, stream);
-    return launch_grouped_t<G, 16, 4>(w, m, k, q, ds, g, out, narrow_waves16(items * ((m + 15) / 16), k), stream);
+    return launch_grouped_t<G, 16, 4>(w, m, k, q, ds, g, out, std::min(4, ((k >> 8) + 1) / 2), stream);
 }
 
 }  // namespace
