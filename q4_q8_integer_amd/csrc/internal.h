@@ -163,15 +163,11 @@ constexpr int kQ6kFewMaxN = 64;
 // of the experts with g.lo .. g.hi slots.  tokens_per_item: the most slots
 // one item should hold, rounded up to what the kernel has.
 struct Groups;
-hipError_t launch_narrow_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                                 const OutEpi& out, int tokens_per_item, hipStream_t stream);
 hipError_t launch_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
                               const OutEpi& out, int tokens_per_item, hipStream_t stream);
-hipError_t launch_q6k_gemv_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                                   const Groups& g, const OutEpi& out, int tokens_per_item, hipStream_t stream);
 constexpr int kGroupFewMaxN = 16;
-hipError_t launch_few_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                              const OutEpi& out, hipStream_t stream);
+hipError_t launch_few_grouped(bool q6k, const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
+                              const Groups& g, const OutEpi& out, hipStream_t stream);
 hipError_t launch_q6k_few_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                                   const Groups& g, const OutEpi& out, hipStream_t stream);
 hipError_t launch_q6k_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,

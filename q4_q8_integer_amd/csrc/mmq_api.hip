@@ -378,16 +378,15 @@ int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t
         g.hi = (int)most;
         return g.lo <= slots;
     };
-    const int per = slots <= 4 || mean < 1 ? 4 : mean < 4 ? 8 : 16;
     if (q6k) {
-        if ((slots <= mmq::kQ6kGemvMaxN || mean < 4) && take(mmq::kQ6kGemvMaxN))
-            rc = hip_status(mmq::launch_q6k_gemv_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, per, stream));
+        if (take(mmq::kGroupFewMaxN))
+            rc = hip_status(mmq::launch_few_grouped(true, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
         if (rc == MMQ_OK && take(mmq::kQ6kFewMaxN))
             rc = hip_status(mmq::launch_q6k_few_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
         if (rc == MMQ_OK && take(slots))
             rc = hip_status(mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
     } else {
-        if (take(mmq::kGroupFewMaxN)) rc = hip_status(mmq::launch_few_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
+        if (take(mmq::kGroupFewMaxN)) rc = hip_status(mmq::launch_few_grouped(false, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
         if (rc == MMQ_OK && take(slots))
             rc = hip_status(mmq::launch_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, mean < 96 ? 64 : 128, stream));
     }

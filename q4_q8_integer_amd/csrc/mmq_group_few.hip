@@ -1,39 +1,43 @@
-// mmq_group_few.hip - q4_K x q8 products grouped by expert, for experts of up
-// to 64 slots: 16x16x32 int8 MFMA, the active experts' weights streamed once.
+// mmq_group_few.hip - products grouped by expert, for experts of few slots:
+// 16x16x32 int8 MFMA, the active experts' weights streamed once.
 //
-// Method as in the other kernels: exact integer dots of a chunk (k = 32), then
-// the two-term fold.
+// Method as in the other kernels: exact integer dots of a chunk (k = 32; in
+// q6_K of its two scale groups, k = 16), then the fold.
 //
 //   * A is 16 tokens, B 16 weight rows: lane l supplies k = 8 (l / 16) .. +7 of
 //     the chunk for token / row l % 16, and holds the results of row l % 16
 //     with tokens 4 (l / 16) .. +3, so the weight scales are per-lane values.
 //     Unused tokens of a tile are padding: the stream of weights leaves the
 //     vector unit time for them.
-//   * The MFMA starts from the bits of 1.5 * 2^23, so its result D read as
-//     float32 is 1.5 * 2^23 + D exactly; fma(sc, that, -1.5 * 2^23 * sc) is
+//   * q4_K: the MFMA starts from the bits of 1.5 * 2^23, so its result D read
+//     as float32 is 1.5 * 2^23 + D exactly; fma(sc, that, -1.5 * 2^23 * sc) is
 //     sc * D, exact as |sc * D| < 2^22; then acc_b += da * it, da taken as
 //     binary16 by the mixed-precision multiply-add.  Per super-block out += d *
 //     acc_b, and the min term on v_mfma_f32_16x16x4_f32.
+//   * q6_K: the two groups' dots come from two MFMAs on the same tokens, the
+//     weights of the other group's lanes set to 0 (lanes 0-31 hold the first
+//     group's k); sc0*D0 + sc1*D1 is exact in 24-bit integer operations.
 //   * A workgroup of 8 waves goes over its units, a unit being 128/KS rows of
 //     one item: 8/KS row tiles of 16, KS waves on each that take its
-//     super-blocks in turn.  KS (1, 2, 4 or 8) is the least that gives the
-//     CUs' 4096 waves a tile each, from the number of items, which the kernel
-//     counts itself.  KS > 1 adds the waves' sums through LDS, in wave order.
-//   * A wave's step is one super-block and one tile of 16 tokens.  It reads
-//     its copy of the step (weights, codes, scale words) from its LDS area
-//     into registers, and at once sends the next step's copies into the same
-//     area (buffer loads that write LDS directly, in inline asm outside the
-//     compiler's wait bookkeeping); they are in flight during the arithmetic,
-//     also from one unit to the next.  One area per wave leaves room for 16
-//     waves per CU: with 8 (and two areas) a SIMD's two waves issued vector
+//     super-blocks in turn.  KS > 1 adds the waves' sums through LDS, in wave
+//     order.  The kernel counts the items and chooses KS itself (split()).
+//   * A wave's step is one super-block.  It reads its copy of the step
+//     (weights, codes, scale words) from its LDS area into registers, and at
+//     once sends the next step's copies into the same area (buffer loads that
+//     write LDS directly, in inline asm outside the compiler's wait
+//     bookkeeping); they are in flight during the arithmetic, also from one
+//     unit to the next.  One area per wave leaves room for 16 waves per CU:
+//     with 8 waves and two areas a SIMD's two waves issued vector
 //     instructions at less than half its rate (8 experts of 14336 x 4096, 8
-//     slots each: 99 us, 87 without any copies).
+//     slots each: 99 us, 87 of them without any copies; this kernel 72).
 #include <algorithm>
 
 #include "f16_operand.h"
 #include "group.h"
 #include "internal.h"
 #include "kquant_device.h"
+#include "q6k_device.h"
+#include "q6k_stage.h"
 
 namespace mmq {
 namespace {
@@ -53,12 +57,6 @@ constexpr int kMagicBits = 0x4B400000;
 
 // By value: a bit cast of a vector's element reads its first element.
 __device__ __forceinline__ float as_float(int x) { return __builtin_bit_cast(float, x); }
-
-// A wave's area, by byte offset.  Weights: 16 rows of 144 bytes (9 pieces, an
-// odd number, so 16 rows' reads of one piece meet different banks).  Codes:
-// slot 16t + s holds piece s ^ t of token t.  Words: 8 per token.
-constexpr int kCodes = 16 * kBlockBytes, kWords = kCodes + 16 * 256, kArea = kWords + 16 * 32;
-static_assert(kCodes % 256 == 0 && kArea % 256 == 0, "the codes start on a 256-byte boundary");
 
 typedef __attribute__((address_space(3))) uint8_t* Lds;
 template <class V>
@@ -92,38 +90,221 @@ __device__ __forceinline__ int count_items(const Groups& g) {
     return __builtin_amdgcn_readfirstlane(n);
 }
 
-// The weights of one super-block as a lane's operands.
-struct Weights {
+// ------------------------------------------------------------------- q4_K
+struct Q4k {
+    static constexpr int kBlock = kBlockBytes;
+    // 16 rows of 144 bytes (9 pieces, an odd number, so 16 rows' reads of one
+    // piece meet different banks): two copies and a quarter of one.
+    static constexpr int kRow = kBlockBytes, kBytes = 16 * kRow, kCopies = 3, kLast = 16;
+    // Byte offset in the tile, for super-block 0, of copy c's piece (slot i =
+    // 64c + lane: piece i % 9 of row i / 9; rows past the tile lie past the
+    // resource: zeros, not used).
+    __device__ static uint32_t piece(int c, int lane, int S) {
+        const int i = 64 * c + lane;
+        return (uint32_t)(i / 9) * (uint32_t)(S * kBlock) + 16u * (uint32_t)(i % 9);
+    }
+    __device__ static uint32_t offset(uint32_t piece, int sb) { return piece + (uint32_t)(sb * kBlock); }
+
+    // A super-block's bytes of row r, k = 8kg.. of each chunk, as they are.
+    struct Raw {
+        v4u hdr;
+        v2u qs[4];
+        __device__ __forceinline__ void read(uint32_t area, int r, int kg, int, int) {
+            const uint32_t p = area + kRow * r;
+            hdr = lds_read<v4u>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qs[i] = lds_read<v2u>(p + 16 + 32 * i + 8 * kg);
+        }
+    };
+    __device__ static void patch(uint32_t, uint64_t, int, int, int, int) {}
+
     int64_t b[8];
     uint32_t sc[2];   // eight scale bytes
     float d, bneg[2];
     __device__ __forceinline__ float scale(int c) const { return (float)((sc[c >> 2] >> (8 * (c & 3))) & 0xFFu); }
-    __device__ __forceinline__ void decode(const v4u& hdr, const v2u (&x)[4], int kg) {
+    __device__ __forceinline__ void decode(const Raw& x, int kg) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            b[2 * p] = (int64_t)(((uint64_t)(x[p][1] & 0x0F0F0F0Fu) << 32) | (x[p][0] & 0x0F0F0F0Fu));
-            b[2 * p + 1] = (int64_t)(((uint64_t)((x[p][1] >> 4) & 0x0F0F0F0Fu) << 32) | ((x[p][0] >> 4) & 0x0F0F0F0Fu));
+            const v2u y = x.qs[p];
+            b[2 * p] = (int64_t)(((uint64_t)(y[1] & 0x0F0F0F0Fu) << 32) | (y[0] & 0x0F0F0F0Fu));
+            b[2 * p + 1] = (int64_t)(((uint64_t)((y[1] >> 4) & 0x0F0F0F0Fu) << 32) | ((y[0] >> 4) & 0x0F0F0F0Fu));
         }
         // the 6-bit fields as bytes (packing: kquant_device.h), scales 0-3 and
         // 4-7, mins alike
-        const uint32_t s0 = hdr[1] & 0x3F3F3F3Fu, s1 = (hdr[3] & 0x0F0F0F0Fu) | ((hdr[1] >> 2) & 0x30303030u);
-        const uint32_t m0 = hdr[2] & 0x3F3F3F3Fu, m1 = ((hdr[3] >> 4) & 0x0F0F0F0Fu) | ((hdr[2] >> 2) & 0x30303030u);
-        sc[0] = s0;
-        sc[1] = s1;
-        d = half_lo(hdr[0]);
-        const float dmin = -half_lo(hdr[0] >> 16);
+        const v4u h = x.hdr;
+        sc[0] = h[1] & 0x3F3F3F3Fu;
+        sc[1] = (h[3] & 0x0F0F0F0Fu) | ((h[1] >> 2) & 0x30303030u);
+        const uint32_t m0 = h[2] & 0x3F3F3F3Fu, m1 = ((h[3] >> 4) & 0x0F0F0F0Fu) | ((h[2] >> 2) & 0x30303030u);
+        d = half_lo(h[0]);
+        const float dmin = -half_lo(h[0] >> 16);
         bneg[0] = dmin * (float)((m0 >> (8 * kg)) & 0xFFu);
         bneg[1] = dmin * (float)((m1 >> (8 * kg)) & 0xFFu);
     }
+    // out's part of the super-block: a = the lane's token operands, da(i, c) =
+    // da of token 4 kg + i, own = the words of token r, chunks kg and kg + 4.
+    template <class D>
+    __device__ __forceinline__ v4f fold(const int64_t (&a)[8], const D& da, const uint32_t (&own)[2], int) const {
+        v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f}, part = s;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            part = __builtin_amdgcn_mfma_f32_16x16x4f32(half_lo(own[j]) * (float)(int16_t)(uint16_t)(own[j] >> 16),
+                                                        bneg[j], part, 0, 0, 0);
+        const v4i magic = v4i{kMagicBits, kMagicBits, kMagicBits, kMagicBits};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // four dots before their folds, which then find them done
+            v4i D4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                D4[c] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[4 * h + c], b[4 * h + c], magic, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float f = scale(4 * h + c), kf = -kMagic * f;   // exact: 6 bits times 2
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = fmaf(da(i, 4 * h + c), fmaf(f, as_float(D4[c][i]), kf), s[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[i] = fmaf(d, s[i], part[i]);
+        return part;
+    }
 };
+
+// ------------------------------------------------------------------- q6_K
+struct Q6k {
+    static constexpr int kBlock = kQ6kBlockBytes;
+    // Rows of 14 pieces from the 16-byte boundary at or below the block, and a
+    // padding slot (q6k_stage.h): three copies and three quarters of one.
+    static constexpr int kRow = Seg<1>::kBytes, kBytes = 16 * kRow, kCopies = 4, kLast = 48;
+    static_assert(kBytes == 3 * 1024 + 16 * kLast, "the last copy's lanes");
+    __device__ static uint32_t piece(int c, int lane, int S) {
+        const int i = 64 * c + lane;
+        // the row's bytes and the piece number (its low 4 bits free: rows are
+        // a multiple of 16 bytes only with the block's offset added)
+        return (uint32_t)min(i / Seg<1>::kSlots, 15) * (uint32_t)(S * kBlock) |
+               ((uint32_t)min(i % Seg<1>::kSlots, Seg<1>::kChunks - 1) << 28);
+    }
+    __device__ static uint32_t offset(uint32_t piece, int sb) {
+        return (((piece & 0x0FFFFFFFu) + (uint32_t)(sb * kBlock)) & ~15u) + ((piece >> 28) << 4);
+    }
+
+    struct Raw {
+        uint32_t l0[2][3], l1[2][3], h[2][3], sc[5], d;
+        uint32_t sh;
+        __device__ __forceinline__ void read(uint32_t area, int r, int kg, int S, int sb) {
+            const uint32_t off = ((uint32_t)(r * S + sb) * (uint32_t)kBlock) & 15u;
+            sh = off & 3u;
+            const uint32_t row = area + kRow * r + (off & ~3u), p = row + 8 * kg;
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    l0[g][i] = lds_read<uint32_t>(p + 64 * g + 4 * i);
+                    l1[g][i] = lds_read<uint32_t>(p + 64 * g + 32 + 4 * i);
+                    h[g][i] = lds_read<uint32_t>(p + 128 + 32 * g + 4 * i);
+                }
+#pragma unroll
+            for (int i = 0; i < 5; ++i) sc[i] = lds_read<uint32_t>(row + 192 + 4 * i);
+            d = lds_read<uint32_t>(row + 208);
+        }
+    };
+    // The tile's last bytes, where they end inside a 16-byte piece.
+    __device__ static void patch(uint32_t area, uint64_t base, int rows, int S, int sb, int lane) {
+        const int end = rows * S * kBlock, end16 = end & ~15;
+        if (end16 == end) return;
+        const int ch = (end16 - ((((rows - 1) * S + sb) * kBlock) & ~15)) >> 4;
+        if (lane == 0 && ch >= 0 && ch < Seg<1>::kChunks) {
+            const uint4 v = load_piece(reinterpret_cast<const uint8_t*>(base), end16, end);
+            *(__attribute__((address_space(3))) v4u*)(uintptr_t)(area + (uint32_t)((rows - 1) * kRow + 16 * ch)) =
+                v4u{v.x, v.y, v.z, v.w};
+        }
+    }
+
+    int64_t b[8];
+    uint32_t sc[4];   // sixteen scale bytes
+    float d;
+    __device__ __forceinline__ void decode(const Raw& x, int) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t l0[2], l1[2], h[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l0[i] = __builtin_amdgcn_alignbyte(x.l0[g][i + 1], x.l0[g][i], x.sh);
+                l1[i] = __builtin_amdgcn_alignbyte(x.l1[g][i + 1], x.l1[g][i], x.sh);
+                h[i] = __builtin_amdgcn_alignbyte(x.h[g][i + 1], x.h[g][i], x.sh);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t c[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    c[i] = q6k::signed_codes(((j & 1) ? l1[i] : l0[i]) >> (4 * (j >> 1)), h[i] >> (2 * j));
+                b[4 * g + j] = (int64_t)(((uint64_t)c[1] << 32) | c[0]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = __builtin_amdgcn_alignbyte(x.sc[i + 1], x.sc[i], x.sh);
+        d = half_lo(x.d >> (8 * x.sh));
+    }
+    template <class D>
+    __device__ __forceinline__ v4f fold(const int64_t (&a)[8], const D& da, const uint32_t (&)[2], int kg) const {
+        v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        const v4i zero = v4i{0, 0, 0, 0};
+        const int64_t lo = kg < 2 ? -1 : 0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {   // two chunks' dots before their folds
+            v4i d0[2], d1[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                d0[c] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[2 * h + c], b[2 * h + c] & lo, zero, 0, 0, 0);
+                d1[c] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[2 * h + c], b[2 * h + c] & ~lo, zero, 0, 0, 0);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int sc0 = (int8_t)(sc[h] >> (16 * c)), sc1 = (int8_t)(sc[h] >> (16 * c + 8));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[i] = fmaf(da(i, 2 * h + c), (float)(__mul24(sc0, d0[c][i]) + __mul24(sc1, d1[c][i])), s[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] *= d;
+        return s;
+    }
+};
+
+// The waves on a row tile: the least time by a model of the work on the
+// busiest CU, its units times a unit's steps and 4/3 of a step for its ends,
+// a quarter more where a CU has one workgroup of 8 waves.  (q4_K, k = 4096,
+// KS = 1 / 2 / 4 / 8: 1792 tiles 21.7 / 20.2 / 21.5 / 21.8 us, 2688 tiles 31.1 /
+// 24.6 / 28.5 us, 7168 tiles 82.5 / 71.8 us.)
+__device__ __forceinline__ int split(int items, int tiles, int S) {
+    int best = 1;
+    uint64_t least = ~0ull;
+#pragma unroll
+    for (int l = 0; 1 << l <= kWaves; ++l) {
+        const uint32_t groups = ((tiles << l) + kWaves - 1) / kWaves;   // units of an item
+        const uint64_t units = (uint64_t)(uint32_t)items * groups;
+        const uint64_t cost =
+            ((units + 255) >> 8) * (uint32_t)(3 * ((S + (1 << l) - 1) >> l) + 4) * (units <= 256 ? 5u : 4u);
+        if ((1 << l) <= S && cost < least) {
+            least = cost;
+            best = 1 << l;
+        }
+    }
+    return best;
+}
 
 // BIG: rows of more than kFlush super-blocks, whose sums move into a second
 // accumulator every kFlush.
-template <bool BIG>
+template <class F, bool BIG>
 __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uint8_t* __restrict__ w,
                                                                        const int8_t* __restrict__ q,
                                                                        const uint32_t* __restrict__ ds, int M, int K,
                                                                        OutEpi out, Groups grp) {
+    // a wave's area: weights; codes, slot 16t + s holding piece s ^ t of token t;
+    // 8 scale words per token
+    constexpr int kCodes = F::kBytes, kWords = kCodes + 16 * 256, kArea = kWords + 16 * 32;
+    static_assert(kCodes % 256 == 0 && kArea % 256 == 0, "the codes start on a 256-byte boundary");
     __shared__ __attribute__((aligned(256))) uint8_t areas[kWaves * kArea];
     __shared__ v4f red[kWaves][64];
     const int lane = threadIdx.x & 63;
@@ -133,20 +314,19 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const int tiles = (M + 15) >> 4;
     const uint32_t area = (uint32_t)(uintptr_t)(Lds)areas + (uint32_t)(wv * kArea);
 
-    // KS waves on a row tile
     const int items = count_items<kTokens>(grp);
-    int KS = 1;
-    while (KS < kWaves && 2 * KS <= S && (int64_t)items * tiles * KS < 256 * kHeld * kWaves) KS *= 2;
+    const int KS = split(items, tiles, S);
     const int per_unit = kWaves / KS, unit_tiles = (tiles + per_unit - 1) / per_unit;
     const int rt = wv / KS, ks = wv - rt * KS;
 
-    // A wave's place in its stream: super-block sb of a row tile of a unit; the
-    // tile's weights as a buffer resource (base, bytes); off, woff: this lane's
+    // A wave's place in its stream: super-block sb of a row tile (its rows from
+    // base) of a unit; off, woff: this lane's
     // copy offsets of the item's tokens' codes and words at super-block 0.
     struct Pos {
         int unit, sb;
         Item it;
-        uint32_t lo, hi, bytes;
+        uint64_t base;
+        int rows;
         uint32_t off[4], woff;
     };
     const auto enter = [&](Pos& x, int unit) {
@@ -157,10 +337,9 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
         if (!x.it.valid) return;
         // past the last tile: its rows again, not stored
         const int row0 = min(ut * per_unit + rt, tiles - 1) * 16;
-        const uint64_t base = reinterpret_cast<uint64_t>(w) + ((uint64_t)x.it.expert * M + row0) * S * kBlockBytes;
-        x.lo = (uint32_t)base;
-        x.hi = (uint32_t)(base >> 32) & 0xFFFFu;
-        x.bytes = (uint32_t)(min(16, M - row0) * S * kBlockBytes);
+        const uint64_t base = reinterpret_cast<uint64_t>(w) + ((uint64_t)x.it.expert * M + row0) * S * F::kBlock;
+        x.base = base;
+        x.rows = min(16, M - row0);
         const TokenRows<Groups> src(grp, x.it, 0);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -176,23 +355,21 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const uint64_t qa = reinterpret_cast<uint64_t>(q), da_ = reinterpret_cast<uint64_t>(ds);
     const u32x4 qrs = {(uint32_t)qa, (uint32_t)(qa >> 32) & 0xFFFFu, q_bytes, (uint32_t)kBufferFlags};
     const u32x4 drs = {(uint32_t)da_, (uint32_t)(da_ >> 32) & 0xFFFFu, q_bytes / 8, (uint32_t)kBufferFlags};
-    // Copy c of a step's weights: slot i = 64c + lane holds piece i % 9 of row
-    // i / 9 (rows past the tile lie past the resource: zeros, not used).
-    uint32_t at[3];
+    uint32_t at[F::kCopies];
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-        const int i = 64 * c + lane;
-        at[c] = (uint32_t)(i / 9) * (uint32_t)(S * kBlockBytes) + 16u * (uint32_t)(i % 9);
-    }
+    for (int c = 0; c < F::kCopies; ++c) at[c] = F::piece(c, lane, S);
     // The copies of one step.  Those of four tokens past the item's last are
     // left out: what the area holds then is computed with and not stored.
     const auto issue = [&](const Pos& ps) {
-        const u32x4 rs = {(uint32_t)__builtin_amdgcn_readfirstlane(ps.lo), (uint32_t)__builtin_amdgcn_readfirstlane(ps.hi),
-                          (uint32_t)__builtin_amdgcn_readfirstlane(ps.bytes), (uint32_t)kBufferFlags};
-        const uint32_t add = (uint32_t)(ps.sb * kBlockBytes), tok = (uint32_t)ps.sb * 256u;
-        lds_copy16(rs, area, (int)(at[0] + add));
-        lds_copy16(rs, area + 1024, (int)(at[1] + add));
-        if (lane < 16) lds_copy16(rs, area + 2048, (int)(at[2] + add));
+        const u32x4 rs = {(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)ps.base),
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(ps.base >> 32) & 0xFFFFu),
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(ps.rows * S * F::kBlock) & ~15u),
+                          (uint32_t)kBufferFlags};
+        const uint32_t tok = (uint32_t)ps.sb * 256u;
+#pragma unroll
+        for (int c = 0; c < F::kCopies - 1; ++c) lds_copy16(rs, area + 1024 * c, (int)F::offset(at[c], ps.sb));
+        if (lane < F::kLast)
+            lds_copy16(rs, area + 1024 * (F::kCopies - 1), (int)F::offset(at[F::kCopies - 1], ps.sb));
         if (lane < 32) lds_copy16(drs, area + kWords, (int)(ps.woff + (tok >> 3)));
         lds_copy16(qrs, area + kCodes, (int)(ps.off[0] + tok));
 #pragma unroll
@@ -204,7 +381,7 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     // piece 2c + (kg >> 1), in slot 16 r + (piece ^ r): bits 5-7 of the address
     // are c ^ (r >> 1).
     const uint32_t arow = area + kCodes + 256 * r + 32 * (r >> 1) + 16 * ((kg >> 1) ^ (r & 1)) + 8 * (kg & 1);
-    const uint32_t wrow = area + kBlockBytes * r, drow = area + kWords + 128 * kg;
+    const uint32_t drow = area + kWords + 128 * kg;
 
     v4f acc = v4f{0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
     Pos cur, nxt;
@@ -231,41 +408,22 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
             }
 #pragma unroll
         for (int h = 0; h < 2; ++h) own[h] = lds_read<uint32_t>(area + kWords + 32 * r + 4 * kg + 16 * h);
-        const v4u hdr = lds_read<v4u>(wrow);
-        v2u qs[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) qs[p] = lds_read<v2u>(wrow + 16 + 32 * p + 8 * kg);
+        F::patch(area, cur.base, cur.rows, S, cur.sb, lane);
+        typename F::Raw raw;
+        raw.read(area, r, kg, S, cur.sb);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         if (nxt.it.valid) issue(nxt);   // the next step into it
         __builtin_amdgcn_sched_barrier(0);
-        Weights x;
-        x.decode(hdr, qs, kg);
-        // out's part of the super-block
-        v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f}, part = s;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            part = __builtin_amdgcn_mfma_f32_16x16x4f32(half_lo(own[j]) * (float)(int16_t)(uint16_t)(own[j] >> 16),
-                                                        x.bneg[j], part, 0, 0, 0);
-        const v4i magic = v4i{kMagicBits, kMagicBits, kMagicBits, kMagicBits};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {   // four dots before their folds, which then find them done
-            v4i D[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                D[c] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[4 * h + c], x.b[4 * h + c], magic, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float sc = x.scale(4 * h + c), ksc = -kMagic * sc;   // exact: 6 bits times 2
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t dd = da[i][2 * h + (c >> 1)];
-                    s[i] = fmaf(half_lo((c & 1) ? dd >> 16 : dd), fmaf(sc, as_float(D[c][i]), ksc), s[i]);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += fmaf(x.d, s[i], part[i]);
+        F x;
+        x.decode(raw, kg);
+        acc += x.fold(
+            a,
+            [&](int i, int c) {
+                const uint32_t dd = da[i][c >> 1];
+                return half_lo((c & 1) ? dd >> 16 : dd);
+            },
+            own, kg);
         if (BIG && done % kFlush == 0) {
             acc2 += acc;
             acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -313,15 +471,15 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
 
 }  // namespace
 
-hipError_t launch_few_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                              const OutEpi& out, hipStream_t stream) {
+hipError_t launch_few_grouped(bool q6k, const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
+                              const Groups& g, const OutEpi& out, hipStream_t stream) {
     const int64_t units = most_items(g.experts, g.slots, g.lo, g.hi, kTokens) * ((m + 15) / 16);
     const dim3 grid((unsigned)std::min<int64_t>(units, 256 * kHeld)), block(kNT);
-    if ((k >> 8) > kFlush)
-        hipLaunchKernelGGL((mmq_group_few_kernel<true>), grid, block, 0, stream, w, q, ds, m, k, out, g);
-    else
-        hipLaunchKernelGGL((mmq_group_few_kernel<false>), grid, block, 0, stream, w, q, ds, m, k, out, g);
-    return hipGetLastError();
+    const bool big = (k >> 8) > kFlush;
+    const void* f = q6k ? (big ? (const void*)mmq_group_few_kernel<Q6k, true> : (const void*)mmq_group_few_kernel<Q6k, false>)
+                        : (big ? (const void*)mmq_group_few_kernel<Q4k, true> : (const void*)mmq_group_few_kernel<Q4k, false>);
+    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&k, (void*)&out, (void*)&g};
+    return hipLaunchKernel(f, grid, block, args, 0, stream);
 }
 
 }  // namespace mmq

@@ -53,7 +53,6 @@
 //     rounding error of very long rows (k up to 2^24) within the float32 bar.
 #include <algorithm>
 
-#include "group.h"
 #include "internal.h"
 #include "kquant_device.h"
 
@@ -197,22 +196,26 @@ __device__ __forceinline__ void compute_step(const uint8_t* area, bool live, int
     }
 }
 
-// One tile of RT rows from row0 on, for the N tokens of rows (N <= 4G).
-// area0, area1: two areas per wave, as two arrays: the copies into one are in
-// flight while the other is read, and the compiler can tell them apart.
-template <int G, class O, int RT, class Grp>
-__device__ __forceinline__ void narrow_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
-                                            const uint32_t* __restrict__ ds, const TokenRows<Grp>& src,
-                                            uint32_t q_rows, int M, int N, int K, int row0, const O& out,
-                                            uint8_t (*area0)[Area<G, RT>::kBytes],
-                                            uint8_t (*area1)[Area<G, RT>::kBytes]) {
+template <int G, class O, int RT, int WM>
+__global__ __launch_bounds__(64 * WM) void mmq_narrow_kernel(const uint8_t* __restrict__ w,
+                                                             const int8_t* __restrict__ q,
+                                                             const uint32_t* __restrict__ ds,
+                                                             int M, int N, int K,
+                                                             O out) {
+    typedef Area<G, RT> A;
     typedef Tile<RT> T;
     constexpr int kS = T::kSlots;
+    // Two areas per wave, as two arrays: the copies into one are in flight
+    // while the other is read, and the compiler can tell them apart.
+    __shared__ __attribute__((aligned(16))) uint8_t area0[WM][A::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t area1[WM][A::kBytes];
+
     const int W = blockDim.x >> 6;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
     const int r = lane & (RT - 1), s = (lane >> 4) & (kS - 1), h = lane >> 5;
     const int ti = lane & 3;     // the lane's token in a group (A operand)
+    const int row0 = blockIdx.x * RT;
     const int rows = min(RT, M - row0);
     const int S = K >> 8, C = K >> 5;
     // Interleaved: wave wv takes the steps wv, wv + W, wv + 2W, ..., so the
@@ -235,10 +238,10 @@ __device__ __forceinline__ void narrow_tile(const uint8_t* __restrict__ w, const
     const int64_t row_bytes = (int64_t)S * kBlockBytes;
     cp.wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(w) + row0 * row_bytes, 0, (int)(rows * row_bytes),
                                               kBufferFlags);
-    cp.qr = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(q), 0, (int)(q_rows * (uint32_t)K), kBufferFlags);
-    cp.dr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(ds), 0, (int)(q_rows * (uint32_t)(C * 4)), kBufferFlags);
+    cp.qr = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(q), 0, N * K, kBufferFlags);
+    cp.dr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(ds), 0, N * C * 4, kBufferFlags);
 #pragma unroll
-    for (int c = 0; c < Area<G, RT>::kWLoads; ++c) {
+    for (int c = 0; c < A::kWLoads; ++c) {
         const int i = 64 * c + lane, wrow = i / T::kRowPieces;
         const int pc = T::wslot(wrow, i % T::kRowPieces);
         const int pv = pc < 9 * kS ? pc : 0;
@@ -249,12 +252,12 @@ __device__ __forceinline__ void narrow_tile(const uint8_t* __restrict__ w, const
     for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int sl = 0; sl < kS; ++sl)
-            cp.tok[g][sl] = src.row(4 * g + (lane >> 4)) * (uint32_t)K +
+            cp.tok[g][sl] = (uint32_t)min(4 * g + (lane >> 4), N - 1) * (uint32_t)K +
                             16u * ((lane & 15) ^ (2 * ((lane >> 4) + 4 * sl)));
     {
         const int wrr = min(lane >> 1, 4 * kS * G - 1);   // row R = 4 kSlots g + 4s + i
         const int tok = 4 * (wrr / (4 * kS)) + (wrr & 3);
-        cp.word = src.row(tok) * (uint32_t)(C * 4) + 16u * (lane & 1);
+        cp.word = (uint32_t)min(tok, N - 1) * (uint32_t)(C * 4) + 16u * (lane & 1);
         cp.word_sl = (wrr >> 2) & (kS - 1);
     }
 
@@ -319,102 +322,37 @@ __device__ __forceinline__ void narrow_tile(const uint8_t* __restrict__ w, const
     }
 }
 
-template <int G, class O, int RT, int WM, class Grp>
-__global__ __launch_bounds__(64 * WM) void mmq_narrow_kernel(const uint8_t* __restrict__ w,
-                                                             const int8_t* __restrict__ q,
-                                                             const uint32_t* __restrict__ ds,
-                                                             int M, int N, int K,
-                                                             O out, Grp grp) {
-    typedef Area<G, RT> A;
-    __shared__ __attribute__((aligned(16))) uint8_t area0[WM][A::kBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t area1[WM][A::kBytes];
-    if constexpr (!Grp::kOn) {
-        narrow_tile<G, O, RT, Grp>(w, q, ds, TokenRows<Grp>(grp, Item{}, N), (uint32_t)N, M, N, K, blockIdx.x * RT, out,
-                                   area0, area1);
-    } else {
-        // tile i: rows (i % tiles) * RT .. of item i / tiles
-        const int tiles = (M + RT - 1) / RT;
-        for (int i = blockIdx.x;; i += gridDim.x) {
-            const Item it = find_item<4 * G>(grp, i / tiles);
-            if (!it.valid) return;   // the same for every wave
-            O o = out;
-            o.advance(it.start);
-            if (o.bias) o.bias += (int64_t)it.expert * M;
-            narrow_tile<G, O, RT, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kBlockBytes, q, ds,
-                                       TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, it.count, K,
-                                       i % tiles * RT, o, area0, area1);
-            __syncthreads();   // the sums are read before the areas are filled again
-        }
-    }
-}
-
 template <int G, int RT, int WM>
-hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                    const Out& out, int W, hipStream_t stream) {
+hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, const Out& out,
+                    int W, hipStream_t stream) {
     return with_out(out, [&](auto o) {
-        NoGroups none;
-        void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&o, (void*)&none};
-        return hipLaunchKernel((const void*)mmq_narrow_kernel<G, decltype(o), RT, WM, NoGroups>,
+        void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&o};
+        return hipLaunchKernel((const void*)mmq_narrow_kernel<G, decltype(o), RT, WM>,
                                dim3((unsigned)((m + RT - 1) / RT)), dim3(64 * W), args, 0, stream);
     });
-}
-
-// Waves per workgroup of 16-row tiles: up to 4, about 8192 in all over wgs
-// tiles, preferring a count that divides the steps evenly.
-int narrow_waves16(int64_t wgs, int k) {
-    const int steps = ((k >> 8) + 1) / 2;
-    const int wmax = (int)std::max<int64_t>(1, std::min<int64_t>({4, steps, (8192 + wgs - 1) / wgs}));
-    for (int c = wmax; c * 2 > wmax; --c)
-        if (steps % c == 0) return c;
-    return wmax;
 }
 
 // Tile and waves per workgroup.  A wave's two areas take 14 to 28 KiB of
 // LDS (5 KiB of weights, 1 (32-row tiles) or 2 KiB of token rows per group
 // and 1 KiB of scale words, twice), so two 4-wave or one 8-wave workgroup
-// fit a CU.  32-row tiles as narrow_waves32 says; otherwise 16-row tiles.
+// fit a CU.  32-row tiles as narrow_waves32 says; otherwise 16-row tiles
+// with up to 4 waves, about 8192 waves in all, preferring a count that
+// divides the steps evenly.
 template <int G>
-hipError_t launch_g(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
-                    const Out& out, hipStream_t stream) {
+hipError_t launch_g(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, const Out& out,
+                    hipStream_t stream) {
     const int w32 = narrow_waves32(m, k);
     if (w32 == 4) return launch_t<G, 32, 4>(w, m, k, q, ds, n, out, 4, stream);
     if (w32 == 8) return launch_t<G, 32, 8>(w, m, k, q, ds, n, out, 8, stream);
-    const int W = narrow_waves16((m + 15) / 16, k);
+    const int wgs = (m + 15) / 16, steps = ((k >> 8) + 1) / 2;
+    const int wmax = (int)std::max<int64_t>(1, std::min<int64_t>({4, steps, (8192 + wgs - 1) / wgs}));
+    int W = wmax;
+    for (int c = wmax; c * 2 > wmax; --c)
+        if (steps % c == 0) { W = c; break; }
     return launch_t<G, 16, 4>(w, m, k, q, ds, n, out, W, stream);
 }
 
-// The grouped launch: as many workgroups as the CUs hold at once (by LDS), or
-// as there can be tiles.
-template <int G, int RT, int WM>
-hipError_t launch_grouped_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                            const OutEpi& out, int W, hipStream_t stream) {
-    const int64_t tiles = most_items(g.experts, g.slots, g.lo, g.hi, 4 * G) * ((m + RT - 1) / RT);
-    const int64_t held = 256 * (160 * 1024 / (2 * WM * Area<G, RT>::kBytes));
-    int n = 0;
-    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&n, (void*)&k, (void*)&out, (void*)&g};
-    return hipLaunchKernel((const void*)mmq_narrow_kernel<G, OutEpi, RT, WM, Groups>,
-                           dim3((unsigned)std::min(tiles, held)), dim3(64 * W), args, 0, stream);
-}
-
-// Layout as for one matrix of the rows of every expert that can be active.
-template <int G>
-hipError_t launch_grouped_g(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                            const OutEpi& out, hipStream_t stream) {
-    const int64_t items = most_items(g.experts, g.slots, g.lo, g.hi, 4 * G);
-    const int w32 = narrow_waves32(items * ((m + 31) / 32 * 32), k);
-    if (w32 == 4) return launch_grouped_t<G, 32, 4>(w, m, k, q, ds, g, out, 4, stream);
-    if (w32 == 8) return launch_grouped_t<G, 32, 8>(w, m, k, q, ds, g, out, 8, stream);
-    return launch_grouped_t<G, 16, 4>(w, m, k, q, ds, g, out, std::min(4, ((k >> 8) + 1) / 2), stream);
-}
-
 }  // namespace
-
-hipError_t launch_narrow_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                                 const OutEpi& out, int tokens_per_item, hipStream_t stream) {
-    return tokens_per_item <= 4   ? launch_grouped_g<1>(w, m, k, q, ds, g, out, stream)
-           : tokens_per_item <= 8 ? launch_grouped_g<2>(w, m, k, q, ds, g, out, stream)
-                                  : launch_grouped_g<4>(w, m, k, q, ds, g, out, stream);
-}
 
 hipError_t launch_mmq_fp32_narrow(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
                                   const Out& out, hipStream_t stream) {

@@ -30,7 +30,6 @@
 //     row by a butterfly, then the waves in index order).
 #include <algorithm>
 
-#include "group.h"
 #include "internal.h"
 #include "kquant_device.h"
 #include "q6k_device.h"
@@ -117,24 +116,6 @@ __device__ __forceinline__ void stage_issue(const Tile& tl, int S, int s, int la
     }
 }
 
-// The row of q of each of a tile's N tokens: token t itself, or in a grouped
-// call the row of the item's slot (slots past the item repeat its last one).
-template <int N, class Grp>
-struct Tokens {
-    __device__ Tokens(const Grp&, const Item&) {}
-    __device__ __forceinline__ int64_t row(int t) const { return t; }
-};
-template <int N>
-struct Tokens<N, Groups> {
-    uint32_t at[N];
-    __device__ Tokens(const Groups& g, const Item& it) {
-        const TokenRows<Groups> src(g, it, 0);
-#pragma unroll
-        for (int t = 0; t < N; ++t) at[t] = __builtin_amdgcn_readfirstlane(src.row(t));
-    }
-    __device__ __forceinline__ int64_t row(int t) const { return at[t]; }
-};
-
 // The activations of one wave step, as one lane holds them: its token dword
 // and scale word of every slot.
 template <int N, int SW>
@@ -144,10 +125,10 @@ struct Fetch {
 
 // Issue the activation loads of the step at super-block s (slots past the
 // wave's range re-read its last block and are not used).
-template <int N, int SW, class Grp>
+template <int N, int SW>
 __device__ __forceinline__ void fetch_step(Fetch<N, SW>& f, const int8_t* __restrict__ q,
-                                           const uint32_t* __restrict__ ds, const Tokens<N, Grp>& tk, int K, int C,
-                                           int s, int last, int h, int e, int r) {
+                                           const uint32_t* __restrict__ ds, int K, int C, int s,
+                                           int last, int h, int e, int r) {
 #pragma unroll
     for (int j = 0; j < SW; ++j) {
         const int sb = min(s + j, last);
@@ -155,8 +136,8 @@ __device__ __forceinline__ void fetch_step(Fetch<N, SW>& f, const int8_t* __rest
         const int64_t woff = (int64_t)sb * 8 + 4 * h + (r & 3);
 #pragma unroll
         for (int t = 0; t < N; ++t) {
-            f.tq[t][j] = q6k::ld32(reinterpret_cast<const uint8_t*>(q) + tk.row(t) * K + toff);
-            f.tw[t][j] = ds[tk.row(t) * C + woff];
+            f.tq[t][j] = q6k::ld32(reinterpret_cast<const uint8_t*>(q) + (int64_t)t * K + toff);
+            f.tw[t][j] = ds[(int64_t)t * C + woff];
         }
     }
 }
@@ -208,17 +189,20 @@ __device__ __forceinline__ void compute_step(const Fetch<N, SW>& f, const uint8_
 
 // PF: two LDS areas per wave, the next step's copy (and activation loads)
 // in flight while a step computes.
-// One tile of 16 rows from row0 on, for the first `toks` of the N tokens tk.
-// seg: W x (PF ? 2 : 1) x Seg<SW>::kArea bytes of LDS.
-template <int N, int SW, bool PF, class O, class Grp>
-__device__ __forceinline__ void q6k_gemv_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
-                                              const uint32_t* __restrict__ ds, const Tokens<N, Grp>& tk, int toks,
-                                              int M, int K, int row0, const O& out, uint8_t* seg,
-                                              float (*red)[N][16]) {
+template <int N, int SW, bool PF, class O>
+__global__ __launch_bounds__(64 * kMaxWaves) void mmq_q6k_gemv_kernel(const uint8_t* __restrict__ w,
+                                                                      const int8_t* __restrict__ q,
+                                                                      const uint32_t* __restrict__ ds,
+                                                                      int M, int K,
+                                                                      O out) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t seg[];   // W x (PF ? 2 : 1) x Seg<SW>::kArea
+    __shared__ float red[kMaxWaves][N][16];
+
     const int W = blockDim.x >> 6;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
     const int p = lane >> 4, r = lane & 15, h = p >> 1, e = p & 1;
+    const int row0 = blockIdx.x * 16;
     const int S = K >> 8, C = K >> 5;
     const int sb0 = (int)((int64_t)S * wv / W), sb1 = (int)((int64_t)S * (wv + 1) / W);
     const int64_t rowS = (int64_t)(row0 + r) * S;
@@ -239,7 +223,7 @@ __device__ __forceinline__ void q6k_gemv_tile(const uint8_t* __restrict__ w, con
     if constexpr (PF) {
         Fetch<N, SW> nx;
         if (sb0 < sb1) {
-            fetch_step<N, SW>(nx, q, ds, tk, K, C, sb0, last, h, e, r);
+            fetch_step<N, SW>(nx, q, ds, K, C, sb0, last, h, e, r);
             stage_issue<SW>(tl, S, sb0, lane, lds);
         }
         for (int s = sb0, b = 0; s < sb1; s += SW, b ^= 1) {
@@ -249,7 +233,7 @@ __device__ __forceinline__ void q6k_gemv_tile(const uint8_t* __restrict__ w, con
             stage_patch<SW>(tl, S, s, lane, cur);
             Fetch<N, SW> f = nx;
             if (s + SW < sb1) {
-                fetch_step<N, SW>(nx, q, ds, tk, K, C, s + SW, last, h, e, r);
+                fetch_step<N, SW>(nx, q, ds, K, C, s + SW, last, h, e, r);
                 stage_issue<SW>(tl, S, s + SW, lane, lds + (b ^ 1) * Seg<SW>::kArea);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -260,7 +244,7 @@ __device__ __forceinline__ void q6k_gemv_tile(const uint8_t* __restrict__ w, con
         // before the next step's copy is issued (its math needs them).
         for (int s = sb0; s < sb1; s += SW) {
             Fetch<N, SW> f;
-            fetch_step<N, SW>(f, q, ds, tk, K, C, s, last, h, e, r);
+            fetch_step<N, SW>(f, q, ds, K, C, s, last, h, e, r);
             stage_issue<SW>(tl, S, s, lane, lds);
             __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
             __builtin_amdgcn_sched_barrier(0);
@@ -280,34 +264,7 @@ __device__ __forceinline__ void q6k_gemv_tile(const uint8_t* __restrict__ w, con
         const int t = i >> 4, rr = i & 15;
         float sum = red[0][t][rr];
         for (int v = 1; v < W; ++v) sum += red[v][t][rr];
-        if (t < toks && row0 + rr < M) out.put(t, row0 + rr, sum);
-    }
-}
-
-template <int N, int SW, bool PF, class O, class Grp>
-__global__ __launch_bounds__(64 * kMaxWaves) void mmq_q6k_gemv_kernel(const uint8_t* __restrict__ w,
-                                                                      const int8_t* __restrict__ q,
-                                                                      const uint32_t* __restrict__ ds,
-                                                                      int M, int K,
-                                                                      O out, Grp grp) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t seg[];
-    __shared__ float red[kMaxWaves][N][16];
-    if constexpr (!Grp::kOn) {
-        q6k_gemv_tile<N, SW, PF, O, Grp>(w, q, ds, Tokens<N, Grp>(grp, Item{}), N, M, K, blockIdx.x * 16, out, seg,
-                                         red);
-    } else {
-        // tile i: rows (i % tiles) * 16 .. of item i / tiles
-        const int tiles = (M + 15) / 16;
-        for (int i = blockIdx.x;; i += gridDim.x) {
-            const Item it = find_item<N>(grp, i / tiles);
-            if (!it.valid) return;   // the same for every wave
-            O o = out;
-            o.advance(it.start);
-            if (o.bias) o.bias += (int64_t)it.expert * M;
-            q6k_gemv_tile<N, SW, PF, O, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kQ6kBlockBytes, q, ds,
-                                             Tokens<N, Grp>(grp, it), it.count, M, K, i % tiles * 16, o, seg, red);
-            __syncthreads();   // the sums are read before they are written again
-        }
+        if (row0 + rr < M) out.put(t, row0 + rr, sum);
     }
 }
 
@@ -317,8 +274,8 @@ hipError_t launch_sw(const uint8_t* w, int m, int k, const int8_t* q, const uint
     const int rows = (m + 15) / 16;
     const size_t lds = (size_t)waves * (PF ? 2 : 1) * Seg<SW>::kArea;
     return with_out(out, [&](auto o) {
-        hipLaunchKernelGGL((mmq_q6k_gemv_kernel<N, SW, PF, decltype(o), NoGroups>), dim3(rows), dim3(64 * waves), lds,
-                           stream, w, q, ds, m, k, o, NoGroups{});
+        hipLaunchKernelGGL((mmq_q6k_gemv_kernel<N, SW, PF, decltype(o)>), dim3(rows), dim3(64 * waves), lds, stream,
+                           w, q, ds, m, k, o);
         return hipGetLastError();
     });
 }
@@ -342,39 +299,7 @@ hipError_t launch_n(const uint8_t* w, int m, int k, const int8_t* q, const uint3
     return launch_sw<N, SW, false>(w, m, k, q, ds, out, stream, waves);
 }
 
-// The grouped launch: as many workgroups as the CUs hold at once (by LDS and
-// by 8 workgroups of 4 waves each), or as there can be tiles.
-template <int N>
-hipError_t launch_grouped_n(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                            const OutEpi& out, hipStream_t stream) {
-    constexpr int SW = N == 1 ? 2 : 1;
-    const int S = k / 256;
-    const int waves = std::min(S, kMaxWaves);
-    const bool pf = N <= 4 && S / (waves * SW) >= 8;
-    const size_t lds = (size_t)waves * (pf ? 2 : 1) * Seg<SW>::kArea;
-    const int64_t held = 256 * std::min<int64_t>(8, 160 * 1024 / (int64_t)(lds + sizeof(float) * kMaxWaves * N * 16));
-    const int64_t tiles = most_items(g.experts, g.slots, g.lo, g.hi, N) * ((m + 15) / 16);
-    const dim3 grid((unsigned)std::min(tiles, held)), block(64 * waves);
-    if constexpr (N <= 4)
-        if (pf) {
-            hipLaunchKernelGGL((mmq_q6k_gemv_kernel<N, SW, true, OutEpi, Groups>), grid, block, lds, stream, w, q, ds,
-                               m, k, out, g);
-            return hipGetLastError();
-        }
-    hipLaunchKernelGGL((mmq_q6k_gemv_kernel<N, SW, false, OutEpi, Groups>), grid, block, lds, stream, w, q, ds, m, k,
-                       out, g);
-    return hipGetLastError();
-}
-
 }  // namespace
-
-hipError_t launch_q6k_gemv_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
-                                   const Groups& g, const OutEpi& out, int tokens_per_item, hipStream_t stream) {
-    return tokens_per_item <= 1   ? launch_grouped_n<1>(w, m, k, q, ds, g, out, stream)
-           : tokens_per_item <= 2 ? launch_grouped_n<2>(w, m, k, q, ds, g, out, stream)
-           : tokens_per_item <= 4 ? launch_grouped_n<4>(w, m, k, q, ds, g, out, stream)
-                                  : launch_grouped_n<8>(w, m, k, q, ds, g, out, stream);
-}
 
 hipError_t launch_q6k_gemv(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                            int n, const Out& out, hipStream_t stream) {
