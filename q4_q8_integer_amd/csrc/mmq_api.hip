@@ -378,16 +378,16 @@ int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t
         g.hi = (int)most;
         return g.lo <= slots;
     };
-    if (q6k) {
-        if (take(mmq::kGroupFewMaxN))
-            rc = hip_status(mmq::launch_few_grouped(true, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
-        if (rc == MMQ_OK && take(mmq::kQ6kFewMaxN))
-            rc = hip_status(mmq::launch_q6k_few_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
-        if (rc == MMQ_OK && take(slots))
+    // The few-token kernel's one-tile form is 2 to 18% faster than its other one
+    // at 1 or 2 slots per expert and even at 16, where its launch is left out.
+    if (mean < mmq::kGroupFewMaxTile && take(mmq::kGroupFewMaxTile))
+        rc = hip_status(mmq::launch_few_grouped(q6k, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
+    if (rc == MMQ_OK && take(q6k ? mmq::kGroupFewMaxQ6k : mmq::kGroupFewMaxQ4k))
+        rc = hip_status(mmq::launch_few_grouped(q6k, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
+    if (rc == MMQ_OK && take(slots)) {
+        if (q6k)
             rc = hip_status(mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));
-    } else {
-        if (take(mmq::kGroupFewMaxN)) rc = hip_status(mmq::launch_few_grouped(false, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
-        if (rc == MMQ_OK && take(slots))
+        else
             rc = hip_status(mmq::launch_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, mean < 96 ? 64 : 128, stream));
     }
     return rc;

@@ -48,7 +48,6 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8, kHeld = 2;   // waves per workgroup, workgroups per CU
-constexpr int kTokens = 16;            // per item
 constexpr int kNT = 64 * kWaves;
 constexpr int kFlush = 256;      // super-blocks of a wave between accumulator moves (BIG)
 
@@ -62,6 +61,10 @@ typedef __attribute__((address_space(3))) uint8_t* Lds;
 template <class V>
 __device__ __forceinline__ V lds_read(uint32_t at) {
     return *(__attribute__((address_space(3))) const V*)(uintptr_t)at;
+}
+template <class V>
+__device__ __forceinline__ void lds_write(uint32_t at, V v) {
+    *(__attribute__((address_space(3))) V*)(uintptr_t)at = v;
 }
 
 // Barrier of the workgroup for LDS only: copies stay in flight over it.
@@ -214,8 +217,7 @@ struct Q6k {
         const int ch = (end16 - ((((rows - 1) * S + sb) * kBlock) & ~15)) >> 4;
         if (lane == 0 && ch >= 0 && ch < Seg<1>::kChunks) {
             const uint4 v = load_piece(reinterpret_cast<const uint8_t*>(base), end16, end);
-            *(__attribute__((address_space(3))) v4u*)(uintptr_t)(area + (uint32_t)((rows - 1) * kRow + 16 * ch)) =
-                v4u{v.x, v.y, v.z, v.w};
+            lds_write<v4u>(area + (uint32_t)((rows - 1) * kRow + 16 * ch), v4u{v.x, v.y, v.z, v.w});
         }
     }
 
@@ -296,14 +298,16 @@ __device__ __forceinline__ int split(int items, int tiles, int S) {
 
 // BIG: rows of more than kFlush super-blocks, whose sums move into a second
 // accumulator every kFlush.
-template <class F, bool BIG>
+template <class F, int T, bool BIG>
 __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uint8_t* __restrict__ w,
                                                                        const int8_t* __restrict__ q,
                                                                        const uint32_t* __restrict__ ds, int M, int K,
                                                                        OutEpi out, Groups grp) {
     // a wave's area: weights; codes, slot 16t + s holding piece s ^ t of token t;
     // 8 scale words per token
-    constexpr int kCodes = F::kBytes, kWords = kCodes + 16 * 256, kArea = kWords + 16 * 32;
+    // (T > 1: then the row of q of each token of the item)
+    constexpr int kCodes = F::kBytes, kWords = kCodes + 16 * 256, kRows = kWords + 16 * 32;
+    constexpr int kArea = kRows + (T > 1 ? (64 * T + 255) / 256 * 256 : 0);
     static_assert(kCodes % 256 == 0 && kArea % 256 == 0, "the codes start on a 256-byte boundary");
     __shared__ __attribute__((aligned(256))) uint8_t areas[kWaves * kArea];
     __shared__ v4f red[kWaves][64];
@@ -314,16 +318,16 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const int tiles = (M + 15) >> 4;
     const uint32_t area = (uint32_t)(uintptr_t)(Lds)areas + (uint32_t)(wv * kArea);
 
-    const int items = count_items<kTokens>(grp);
+    const int items = count_items<16 * T>(grp);
     const int KS = split(items, tiles, S);
     const int per_unit = kWaves / KS, unit_tiles = (tiles + per_unit - 1) / per_unit;
     const int rt = wv / KS, ks = wv - rt * KS;
 
-    // A wave's place in its stream: super-block sb of a row tile (its rows from
-    // base) of a unit; off, woff: this lane's
+    // A wave's place in its stream: tile tt of 16 tokens, super-block sb of a
+    // row tile (its rows from base) of a unit; off, woff (T = 1): this lane's
     // copy offsets of the item's tokens' codes and words at super-block 0.
     struct Pos {
-        int unit, sb;
+        int unit, sb, tt;
         Item it;
         uint64_t base;
         int rows;
@@ -332,8 +336,9 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const auto enter = [&](Pos& x, int unit) {
         x.unit = unit;
         x.sb = ks;
+        x.tt = 0;
         const int item = unit / unit_tiles, ut = unit - item * unit_tiles;
-        x.it = find_item<kTokens>(grp, item);
+        x.it = find_item<16 * T>(grp, item);
         if (!x.it.valid) return;
         // past the last tile: its rows again, not stored
         const int row0 = min(ut * per_unit + rt, tiles - 1) * 16;
@@ -341,12 +346,17 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
         x.base = base;
         x.rows = min(16, M - row0);
         const TokenRows<Groups> src(grp, x.it, 0);
+        if constexpr (T == 1) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            x.off[c] = src.row(4 * c + kg) * (uint32_t)K + 16u * (uint32_t)(r ^ (4 * c + kg));
-        x.woff = src.row(lane >> 1) * (uint32_t)(K >> 3) + 16u * (uint32_t)(lane & 1);
+            for (int c = 0; c < 4; ++c) x.off[c] = src.row(4 * c + kg) * (uint32_t)K + 16u * (uint32_t)(r ^ (4 * c + kg));
+            x.woff = src.row(lane >> 1) * (uint32_t)(K >> 3) + 16u * (uint32_t)(lane & 1);
+        } else if (lane < 16 * T) {
+            lds_write<uint32_t>(area + kRows + 4 * lane, src.row(lane));
+        }
     };
     const auto advance = [&](Pos& x) {
+        if (T > 1 && 16 * ++x.tt < x.it.count) return;
+        x.tt = 0;
         x.sb += KS;
         if (x.sb >= S) enter(x, x.unit + gridDim.x);
     };
@@ -356,8 +366,11 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const u32x4 qrs = {(uint32_t)qa, (uint32_t)(qa >> 32) & 0xFFFFu, q_bytes, (uint32_t)kBufferFlags};
     const u32x4 drs = {(uint32_t)da_, (uint32_t)(da_ >> 32) & 0xFFFFu, q_bytes / 8, (uint32_t)kBufferFlags};
     uint32_t at[F::kCopies];
+    const auto pieces = [&](int ln) {
 #pragma unroll
-    for (int c = 0; c < F::kCopies; ++c) at[c] = F::piece(c, lane, S);
+        for (int c = 0; c < F::kCopies; ++c) at[c] = F::piece(c, ln, S);
+    };
+    if constexpr (T == 1) pieces(lane);
     // The copies of one step.  Those of four tokens past the item's last are
     // left out: what the area holds then is computed with and not stored.
     const auto issue = [&](const Pos& ps) {
@@ -366,15 +379,30 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(ps.rows * S * F::kBlock) & ~15u),
                           (uint32_t)kBufferFlags};
         const uint32_t tok = (uint32_t)ps.sb * 256u;
+        if (T == 1 || ps.tt == 0) {
+            if constexpr (T > 1) pieces(opaque(lane));   // no registers between the copies
 #pragma unroll
-        for (int c = 0; c < F::kCopies - 1; ++c) lds_copy16(rs, area + 1024 * c, (int)F::offset(at[c], ps.sb));
-        if (lane < F::kLast)
-            lds_copy16(rs, area + 1024 * (F::kCopies - 1), (int)F::offset(at[F::kCopies - 1], ps.sb));
-        if (lane < 32) lds_copy16(drs, area + kWords, (int)(ps.woff + (tok >> 3)));
-        lds_copy16(qrs, area + kCodes, (int)(ps.off[0] + tok));
+            for (int c = 0; c < F::kCopies - 1; ++c) lds_copy16(rs, area + 1024 * c, (int)F::offset(at[c], ps.sb));
+            if (lane < F::kLast)
+                lds_copy16(rs, area + 1024 * (F::kCopies - 1), (int)F::offset(at[F::kCopies - 1], ps.sb));
+        }
+        uint32_t off[4], woff;
+        if constexpr (T == 1) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) off[c] = ps.off[c];
+            woff = ps.woff;
+        } else {
+            const uint32_t row = area + kRows + 64 * ps.tt;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                off[c] = lds_read<uint32_t>(row + 16 * c + 4 * kg) * (uint32_t)K + 16u * (uint32_t)(r ^ (4 * c + kg));
+            woff = lds_read<uint32_t>(row + 4 * ((lane >> 1) & 15)) * (uint32_t)(K >> 3) + 16u * (uint32_t)(lane & 1);
+        }
+        if (lane < 32) lds_copy16(drs, area + kWords, (int)(woff + (tok >> 3)));
+        lds_copy16(qrs, area + kCodes, (int)(off[0] + tok));
 #pragma unroll
         for (int c = 1; c < 4; ++c)
-            if (4 * c < ps.it.count) lds_copy16(qrs, area + kCodes + 1024 * c, (int)(ps.off[c] + tok));
+            if (16 * ps.tt + 4 * c < ps.it.count) lds_copy16(qrs, area + kCodes + 1024 * c, (int)(off[c] + tok));
     };
 
     // Where this lane reads: token r's bytes 32c + 8kg of the super-block are
@@ -383,14 +411,17 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const uint32_t arow = area + kCodes + 256 * r + 32 * (r >> 1) + 16 * ((kg >> 1) ^ (r & 1)) + 8 * (kg & 1);
     const uint32_t drow = area + kWords + 128 * kg;
 
-    v4f acc = v4f{0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
+    v4f acc[T], acc2[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) acc[j] = acc2[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    F x;
     Pos cur, nxt;
     enter(cur, blockIdx.x);
     if (!cur.it.valid) return;   // the same for every wave
     issue(cur);
     nxt = cur;
     advance(nxt);
-    for (int done = 1;; ++done) {
+    for (int done = 0;;) {
         __builtin_amdgcn_s_waitcnt(kWaitVmcnt(0));
         asm volatile("" ::: "memory");
         // the step out of the area
@@ -408,59 +439,77 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
             }
 #pragma unroll
         for (int h = 0; h < 2; ++h) own[h] = lds_read<uint32_t>(area + kWords + 32 * r + 4 * kg + 16 * h);
-        F::patch(area, cur.base, cur.rows, S, cur.sb, lane);
         typename F::Raw raw;
-        raw.read(area, r, kg, S, cur.sb);
+        if (T == 1 || cur.tt == 0) {
+            F::patch(area, cur.base, cur.rows, S, cur.sb, lane);
+            raw.read(area, r, kg, S, cur.sb);
+            if constexpr (T > 1) x.decode(raw, kg);
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         if (nxt.it.valid) issue(nxt);   // the next step into it
         __builtin_amdgcn_sched_barrier(0);
-        F x;
-        x.decode(raw, kg);
-        acc += x.fold(
+        if (T == 1 || cur.tt == 0) {
+            if constexpr (T == 1) x.decode(raw, kg);
+            if (BIG && done++ == kFlush) {
+                done = 1;
+#pragma unroll
+                for (int j = 0; j < T; ++j) {
+                    acc2[j] += acc[j];
+                    acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+            }
+        }
+        const v4f part = x.fold(
             a,
             [&](int i, int c) {
                 const uint32_t dd = da[i][c >> 1];
                 return half_lo((c & 1) ? dd >> 16 : dd);
             },
             own, kg);
-        if (BIG && done % kFlush == 0) {
-            acc2 += acc;
-            acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            if (T == 1 || cur.tt == j) acc[j] += part;
         if (!nxt.it.valid || nxt.unit != cur.unit) {
             // The unit's end: the KS waves of a row tile are added.
-            v4f sum = BIG ? acc2 + acc : acc;
-            int tile = cur.unit % unit_tiles * per_unit + rt;
-            bool mine = true;
-            if (KS > 1) {
-                red[wv][lane] = sum;
-                lds_barrier();
-                // wave v < per_unit stores row tile v of the unit
-                mine = wv < per_unit;
-                tile += wv - rt;
-                if (mine) {
-                    sum = red[wv * KS][lane];
+            OutEpi o = out;
+            o.advance(cur.it.start);
+            if (o.bias) o.bias += (int64_t)cur.it.expert * M;
 #pragma unroll 1
-                    for (int v = 1; v < KS; ++v) sum += red[wv * KS + v][lane];
-                }
-                lds_barrier();
-            }
-            const int row = 16 * tile + r;
-            if (mine && row < M) {
-                OutEpi o = out;
-                o.advance(cur.it.start);
-                if (o.bias) o.bias += (int64_t)cur.it.expert * M;
-                // one store in a loop: four of them fill the registers of the
-                // main loop with the epilogue's constants
+            for (int tt = 0; tt < (T == 1 ? 1 : cur.tt + 1); ++tt) {
+                v4f sum;
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+                    if (T == 1 || tt == j) sum = BIG ? acc2[j] + acc[j] : acc[j];
+                int tile = cur.unit % unit_tiles * per_unit + rt;
+                bool mine = true;
+                if (KS > 1) {
+                    red[wv][lane] = sum;
+                    lds_barrier();
+                    // wave v < per_unit stores row tile v of the unit
+                    mine = wv < per_unit;
+                    tile += wv - rt;
+                    if (mine) {
+                        sum = red[wv * KS][lane];
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 4 * kg + i;
-                    if (tok < cur.it.count)
-                        o.put(tok, row, i == 0 ? sum[0] : i == 1 ? sum[1] : i == 2 ? sum[2] : sum[3]);
+                        for (int v = 1; v < KS; ++v) sum += red[wv * KS + v][lane];
+                    }
+                    lds_barrier();
+                }
+                const int row = 16 * tile + r;
+                if (mine && row < M) {
+                    // one store in a loop: four of them fill the registers of
+                    // the main loop with the epilogue's constants
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 16 * tt + 4 * kg + i;
+                        if (tok < cur.it.count)
+                            o.put(tok, row, i == 0 ? sum[0] : i == 1 ? sum[1] : i == 2 ? sum[2] : sum[3]);
+                    }
                 }
             }
-            acc = acc2 = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < T; ++j) acc[j] = acc2[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             done = 0;
         }
         if (!nxt.it.valid) break;
@@ -469,17 +518,24 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     }
 }
 
+template <class F, int T>
+hipError_t launch(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
+                  const OutEpi& out, hipStream_t stream) {
+    const int64_t units = most_items(g.experts, g.slots, g.lo, g.hi, 16 * T) * ((m + 15) / 16);
+    const dim3 grid((unsigned)std::min<int64_t>(units, 256 * kHeld)), block(kNT);
+    const void* f = (k >> 8) > kFlush ? (const void*)mmq_group_few_kernel<F, T, true>
+                                      : (const void*)mmq_group_few_kernel<F, T, false>;
+    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&k, (void*)&out, (void*)&g};
+    return hipLaunchKernel(f, grid, block, args, 0, stream);
+}
+
 }  // namespace
 
 hipError_t launch_few_grouped(bool q6k, const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                               const Groups& g, const OutEpi& out, hipStream_t stream) {
-    const int64_t units = most_items(g.experts, g.slots, g.lo, g.hi, kTokens) * ((m + 15) / 16);
-    const dim3 grid((unsigned)std::min<int64_t>(units, 256 * kHeld)), block(kNT);
-    const bool big = (k >> 8) > kFlush;
-    const void* f = q6k ? (big ? (const void*)mmq_group_few_kernel<Q6k, true> : (const void*)mmq_group_few_kernel<Q6k, false>)
-                        : (big ? (const void*)mmq_group_few_kernel<Q4k, true> : (const void*)mmq_group_few_kernel<Q4k, false>);
-    void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&k, (void*)&out, (void*)&g};
-    return hipLaunchKernel(f, grid, block, args, 0, stream);
+    if (g.hi <= kGroupFewMaxTile)
+        return q6k ? launch<Q6k, 1>(w, m, k, q, ds, g, out, stream) : launch<Q4k, 1>(w, m, k, q, ds, g, out, stream);
+    return q6k ? launch<Q6k, 4>(w, m, k, q, ds, g, out, stream) : launch<Q4k, 4>(w, m, k, q, ds, g, out, stream);
 }
 
 }  // namespace mmq

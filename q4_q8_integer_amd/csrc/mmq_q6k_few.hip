@@ -1,6 +1,6 @@
 // mmq_q6k_few.hip - q6_K x q8 matmul for few tokens (up to 64), on int8 MFMA:
-// the epilogue and the grouped entry points between the dot4 kernel (8
-// tokens) and the binary16-MFMA kernel (128-token tiles).
+// the epilogue entry point between the dot4 kernel (8 tokens) and the
+// binary16-MFMA kernel (128-token tiles).
 //
 // Method as in the other q6_K kernels: per 16-weight group an exact integer
 // dot D = sum (q - 32) * q8, then out[t][o] = sum_g d*sc[g] * da[t, g/2] * D.
@@ -30,10 +30,7 @@
 //
 // Bound by vector issue: per chunk and 16 x 16 outputs 16 operations (and 24
 // per chunk for the decode, shared by the token tiles).
-#include <algorithm>
-
 #include "f16_operand.h"
-#include "group.h"
 #include "internal.h"
 #include "kquant_device.h"
 #include "q6k_device.h"
@@ -59,12 +56,9 @@ struct alignas(16) WaveLds {
     float da[8][16];           // of the step's tile, [chunk][token]
 };
 template <int T>
-struct Lds {
-    union {
-        WaveLds wave[kWaves];
-        v4f red[kWaves][T][64];
-    };
-    uint32_t row[16 * T];      // the row of q of each token
+union Lds {
+    WaveLds wave[kWaves];
+    v4f red[kWaves][T][64];
 };
 
 // Four copies of one KiB: 16 bytes per lane from byte off[c] of rs to
@@ -127,11 +121,13 @@ __device__ __forceinline__ void decode(Weights& x, const uint8_t* row, int off, 
     x.d = half_lo(*reinterpret_cast<const uint32_t*>(row + ((off + 208) & ~3)) >> (8 * sh));
 }
 
-// One tile of 16 rows from row0 on, for the N tokens of `src` (N <= 16 T).
-template <int T, class O, class Grp>
-__device__ __forceinline__ void few_tile(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
-                                         const uint32_t* __restrict__ ds, const TokenRows<Grp>& src, uint32_t q_rows,
-                                         int M, int N, int K, int row0, const O& out, Lds<T>& L) {
+// N <= 16 T.
+template <int T>
+__global__ __launch_bounds__(kNT) void mmq_q6k_few_kernel(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
+                                                          const uint32_t* __restrict__ ds, int M, int N, int K,
+                                                          OutEpi out) {
+    __shared__ Lds<T> L;
+    const int row0 = blockIdx.x * 16;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
     const int r = lane & 15, kg = lane >> 4;
@@ -144,7 +140,7 @@ __device__ __forceinline__ void few_tile(const uint8_t* __restrict__ w, const in
     tl.end = tl.rows * S * kQ6kBlockBytes;
     tl.base = w + (int64_t)row0 * S * kQ6kBlockBytes;
     const u32x4 wrs = resource(tl.base, (uint32_t)tl.end & ~15u);
-    const u32x4 qrs = resource(q, q_rows * (uint32_t)K);
+    const u32x4 qrs = resource(q, (uint32_t)N * (uint32_t)K);
 
     // Copy sources.  Weights: slot i = 64c + lane holds piece i % kSlots of
     // row i / kSlots (the padding slot and those past the 16 rows repeat a
@@ -157,8 +153,6 @@ __device__ __forceinline__ void few_tile(const uint8_t* __restrict__ w, const in
         wrow[c] = min(i / Seg<1>::kSlots, 15) * S;
         wpiece[c] = 16 * min(i % Seg<1>::kSlots, Seg<1>::kChunks - 1);
     }
-    for (int i = threadIdx.x; i < 16 * tiles; i += kNT) L.row[i] = src.row(i);
-    __syncthreads();
     const auto issue_weights = [&](int buf, int sb) {
         uint32_t off[4];
 #pragma unroll
@@ -167,14 +161,13 @@ __device__ __forceinline__ void few_tile(const uint8_t* __restrict__ w, const in
     };
     uint32_t word[2];   // the next step's scale words: token r of its tile, chunks kg and kg + 4
     const auto issue_tokens = [&](int buf, int tt, int sb) {
-        const uint32_t* at = L.row + 16 * tt;
         uint32_t off[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const int tk = 4 * c + kg;
-            off[c] = at[tk] * (uint32_t)K + (uint32_t)sb * 256u + 16u * (uint32_t)(r ^ tk);
+            const int tk = 4 * c + kg;   // tokens past N - 1 repeat it
+            off[c] = (uint32_t)min(16 * tt + tk, N - 1) * (uint32_t)K + (uint32_t)sb * 256u + 16u * (uint32_t)(r ^ tk);
         }
-        const uint32_t* dp = ds + (int64_t)at[r] * C + sb * 8 + kg;
+        const uint32_t* dp = ds + (int64_t)min(16 * tt + r, N - 1) * C + sb * 8 + kg;
 #pragma unroll
         for (int h = 0; h < 2; ++h) word[h] = dp[4 * h];
         copy4(qrs, off, my.tok[buf]);
@@ -263,34 +256,11 @@ __device__ __forceinline__ void few_tile(const uint8_t* __restrict__ w, const in
     }
 }
 
-template <int T, class O, class Grp>
-__global__ __launch_bounds__(kNT) void mmq_q6k_few_kernel(const uint8_t* __restrict__ w, const int8_t* __restrict__ q,
-                                                          const uint32_t* __restrict__ ds, int M, int N, int K, O out,
-                                                          Grp grp) {
-    __shared__ Lds<T> L;
-    if constexpr (!Grp::kOn) {
-        few_tile<T, O, Grp>(w, q, ds, TokenRows<Grp>(grp, Item{}, N), (uint32_t)N, M, N, K, blockIdx.x * 16, out, L);
-    } else {
-        // tile i: rows (i % tiles) * 16 .. of item i / tiles
-        const int tiles = (M + 15) / 16;
-        for (int i = blockIdx.x;; i += gridDim.x) {
-            const Item it = find_item<16 * T>(grp, i / tiles);
-            if (!it.valid) return;   // the same for every wave
-            O o = out;
-            o.advance(it.start);
-            if (o.bias) o.bias += (int64_t)it.expert * M;
-            few_tile<T, O, Grp>(w + (int64_t)it.expert * M * (K >> 8) * kQ6kBlockBytes, q, ds,
-                                TokenRows<Grp>(grp, it, 0), (uint32_t)grp.tokens, M, it.count, K, i % tiles * 16, o, L);
-            __syncthreads();   // the sums are read before the areas are filled again
-        }
-    }
-}
-
 template <int T>
 hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, const OutEpi& out,
                     hipStream_t stream) {
-    hipLaunchKernelGGL((mmq_q6k_few_kernel<T, OutEpi, NoGroups>), dim3((unsigned)((m + 15) / 16)), dim3(kNT), 0, stream,
-                       w, q, ds, m, n, k, out, NoGroups{});
+    hipLaunchKernelGGL((mmq_q6k_few_kernel<T>), dim3((unsigned)((m + 15) / 16)), dim3(kNT), 0, stream,
+                       w, q, ds, m, n, k, out);
     return hipGetLastError();
 }
 
@@ -299,15 +269,6 @@ hipError_t launch_t(const uint8_t* w, int m, int k, const int8_t* q, const uint3
 hipError_t launch_q6k_few(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n, const OutEpi& out,
                           hipStream_t stream) {
     return n <= 16 ? launch_t<1>(w, m, k, q, ds, n, out, stream) : launch_t<4>(w, m, k, q, ds, n, out, stream);
-}
-
-hipError_t launch_q6k_few_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
-                                  const OutEpi& out, hipStream_t stream) {
-    // a workgroup's areas fill a CU
-    const int64_t tiles = most_items(g.experts, g.slots, g.lo, g.hi, 64) * ((m + 15) / 16);
-    hipLaunchKernelGGL((mmq_q6k_few_kernel<4, OutEpi, Groups>), dim3((unsigned)std::min<int64_t>(tiles, 256)), dim3(kNT),
-                       0, stream, w, q, ds, m, 0, k, out, g);
-    return hipGetLastError();
 }
 
 }  // namespace mmq
