@@ -154,14 +154,20 @@ hipError_t launch_q6k_gemv(const uint8_t* w, int m, int k, const int8_t* q, cons
 constexpr int kQ6kGemvMaxN = 8;
 
 // out[t][o] with an epilogue for n <= kQ6kFewMaxN: int8 MFMA on 16-row tiles,
-// the waves of a workgroup split over k (mmq_q6k_few.hip).
+// the waves of a workgroup split over k (mmq_q6k_few.hip); and on the
+// streaming kernel (mmq_group_few.hip).  Where every CU has one tile at most
+// the first is faster (4096 x 11008, 16 / 33 / 64 tokens: 14.6 / 26.6 / 32.1
+// us against 15.0 / 29.0 / 36.2), above that the second, which has 16 waves per
+// CU (8192 x 4096: 13.5 / 22.2 / 26.6 against 11.2 / 21.8 / 27.8; 14336 x 4096:
+// 24.0 / 39.3 / 47.8 against 15.7 / 34.7 / 43.8).
 hipError_t launch_q6k_few(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
                           const OutEpi& out, hipStream_t stream);
-constexpr int kQ6kFewMaxN = 64;
+hipError_t launch_q6k_stream(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
+                             const OutEpi& out, hipStream_t stream);
+constexpr int kQ6kFewMaxN = 64, kQ6kFewMaxM = 4096;
 
-// The matmuls grouped by expert (group.h): the kernels above over the items
-// of the experts with g.lo .. g.hi slots.  tokens_per_item: the most slots
-// one item should hold, rounded up to what the kernel has.
+// The matmuls grouped by expert (group.h), over the items of the experts with
+// g.lo .. g.hi slots.  tokens_per_item: 64 or 128, the slots of one item.
 struct Groups;
 hipError_t launch_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
                               const OutEpi& out, int tokens_per_item, hipStream_t stream);

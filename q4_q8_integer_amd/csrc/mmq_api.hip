@@ -248,8 +248,8 @@ int q6k_fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const u
         if (!threads_ok((m + 15) / 16, 512)) return MMQ_ERR_OVERFLOW;
         rc = check_device();
         if (rc != MMQ_OK) return rc;
-        return hip_status(mmq::launch_q6k_few(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out.epi,
-                                              stream));
+        const auto few = m > mmq::kQ6kFewMaxM ? mmq::launch_q6k_stream : mmq::launch_q6k_few;
+        return hip_status(few(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out.epi, stream));
     }
     FoldLaunch launch = nullptr;
     rc = q6k_fold_launcher(kernel, m, n, &launch);

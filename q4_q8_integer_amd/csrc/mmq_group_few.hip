@@ -1,5 +1,6 @@
-// mmq_group_few.hip - products grouped by expert, for experts of few slots:
-// 16x16x32 int8 MFMA, the active experts' weights streamed once.
+// mmq_group_few.hip - streaming few-token products on 16x16x32 int8 MFMA: the
+// matmuls grouped by expert for experts of few slots, and q6_K with an
+// epilogue for few tokens on tall matrices.
 //
 // Method as in the other kernels: exact integer dots of a chunk (k = 32; in
 // q6_K of its two scale groups, k = 16), then the fold.
@@ -17,20 +18,32 @@
 //   * q6_K: the two groups' dots come from two MFMAs on the same tokens, the
 //     weights of the other group's lanes set to 0 (lanes 0-31 hold the first
 //     group's k); sc0*D0 + sc1*D1 is exact in 24-bit integer operations.
-//   * A workgroup of 8 waves goes over its units, a unit being 128/KS rows of
-//     one item: 8/KS row tiles of 16, KS waves on each that take its
+//   * A workgroup of W waves goes over its units, a unit being 16 W/KS rows of
+//     one item: W/KS row tiles of 16, KS waves on each that take its
 //     super-blocks in turn.  KS > 1 adds the waves' sums through LDS, in wave
 //     order.  The kernel counts the items and chooses KS itself (split()).
-//   * A wave's step is one super-block.  It reads its copy of the step
-//     (weights, codes, scale words) from its LDS area into registers, and at
-//     once sends the next step's copies into the same area (buffer loads that
-//     write LDS directly, in inline asm outside the compiler's wait
-//     bookkeeping); they are in flight during the arithmetic, also from one
-//     unit to the next.  One area per wave leaves room for 16 waves per CU:
-//     with 8 waves and two areas a SIMD's two waves issued vector
-//     instructions at less than half its rate (8 experts of 14336 x 4096, 8
-//     slots each: 99 us, 87 of them without any copies; this kernel 72).
+//   * A wave's step is one super-block and one tile of 16 tokens.  It reads
+//     its copy of the step (weights, codes, scale words) from its LDS area into
+//     registers, and at once sends the next step's copies into the same area
+//     (buffer loads that write LDS directly, in inline asm outside the
+//     compiler's wait bookkeeping); they are in flight during the arithmetic,
+//     also from one unit to the next.  One area per wave leaves room for 16
+//     waves per CU: with 8 waves and two areas a SIMD's two waves issued
+//     vector instructions at less than half its rate (8 experts of 14336 x
+//     4096, 8 slots each: 99 us, 87 of them without any copies; this form 77).
+//   * T = 1 takes items of up to 16 tokens.  T = 4 takes up to 64, the weights
+//     decoded once for all their tiles; its copy addresses are computed anew,
+//     which leaves the loop its registers.
+//
+// Measured (graph of calls): q4_K, 14336 x 4096, 2 / 8 experts of 2 slots 21 /
+// 66-71 us (weights alone at the copy rate 13 / 52), 8 of 16 86, of 32 125; 64
+// experts of 1536 x 4096 at 2 / 16 / 32 slots 58 / 76 / 111 us (44 / 46 / 48);
+// q6_K, 64 of 4096 x 1536 at 1 / 16 / 32 / 64 slots 94 / 106 / 161 / 267 us (64 /
+// 68 / 71 / 79).  Up to 16 slots the weights stream at 3 to 4 TB/s; above, vector
+// issue bounds it (per 16 x 16 outputs and chunk 8 operations in q4_K, 16 in
+// q6_K, and the decode).
 #include <algorithm>
+#include <type_traits>
 
 #include "f16_operand.h"
 #include "group.h"
@@ -47,8 +60,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 8, kHeld = 2;   // waves per workgroup, workgroups per CU
-constexpr int kNT = 64 * kWaves;
 constexpr int kFlush = 256;      // super-blocks of a wave between accumulator moves (BIG)
 
 constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
@@ -72,6 +83,19 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// One item of `tokens` tokens, the rows of q.
+struct OneGroup {
+    int tokens;
+};
+template <int TB>
+__device__ __forceinline__ Item find_item(const OneGroup& g, int i) {
+    return Item{0, 0, g.tokens, i == 0};
+}
+template <int TB>
+__device__ __forceinline__ int count_items(const OneGroup&) {
+    return 1;
 }
 
 // The number of items of a launch (wave-collective).
@@ -279,15 +303,16 @@ struct Q6k {
 // a quarter more where a CU has one workgroup of 8 waves.  (q4_K, k = 4096,
 // KS = 1 / 2 / 4 / 8: 1792 tiles 21.7 / 20.2 / 21.5 / 21.8 us, 2688 tiles 31.1 /
 // 24.6 / 28.5 us, 7168 tiles 82.5 / 71.8 us.)
+template <int W>
 __device__ __forceinline__ int split(int items, int tiles, int S) {
     int best = 1;
     uint64_t least = ~0ull;
 #pragma unroll
-    for (int l = 0; 1 << l <= kWaves; ++l) {
-        const uint32_t groups = ((tiles << l) + kWaves - 1) / kWaves;   // units of an item
+    for (int l = 0; 1 << l <= W; ++l) {
+        const uint32_t groups = ((tiles << l) + W - 1) / W;   // units of an item
         const uint64_t units = (uint64_t)(uint32_t)items * groups;
         const uint64_t cost =
-            ((units + 255) >> 8) * (uint32_t)(3 * ((S + (1 << l) - 1) >> l) + 4) * (units <= 256 ? 5u : 4u);
+            ((units + 255) >> 8) * (uint32_t)(3 * ((S + (1 << l) - 1) >> l) + 4) * (W < 16 && units <= 256 ? 5u : 4u);
         if ((1 << l) <= S && cost < least) {
             least = cost;
             best = 1 << l;
@@ -298,19 +323,20 @@ __device__ __forceinline__ int split(int items, int tiles, int S) {
 
 // BIG: rows of more than kFlush super-blocks, whose sums move into a second
 // accumulator every kFlush.
-template <class F, int T, bool BIG>
-__global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uint8_t* __restrict__ w,
+// W waves per workgroup, 16 / W workgroups per CU.
+template <class F, int T, bool BIG, class Grp, int W>
+__global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t* __restrict__ w,
                                                                        const int8_t* __restrict__ q,
                                                                        const uint32_t* __restrict__ ds, int M, int K,
-                                                                       OutEpi out, Groups grp) {
+                                                                       OutEpi out, Grp grp) {
     // a wave's area: weights; codes, slot 16t + s holding piece s ^ t of token t;
     // 8 scale words per token
     // (T > 1: then the row of q of each token of the item)
     constexpr int kCodes = F::kBytes, kWords = kCodes + 16 * 256, kRows = kWords + 16 * 32;
     constexpr int kArea = kRows + (T > 1 ? (64 * T + 255) / 256 * 256 : 0);
     static_assert(kCodes % 256 == 0 && kArea % 256 == 0, "the codes start on a 256-byte boundary");
-    __shared__ __attribute__((aligned(256))) uint8_t areas[kWaves * kArea];
-    __shared__ v4f red[kWaves][64];
+    __shared__ __attribute__((aligned(256))) uint8_t areas[W * kArea];
+    __shared__ v4f red[W][64];
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
     const int r = lane & 15, kg = lane >> 4;
@@ -319,8 +345,8 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     const uint32_t area = (uint32_t)(uintptr_t)(Lds)areas + (uint32_t)(wv * kArea);
 
     const int items = count_items<16 * T>(grp);
-    const int KS = split(items, tiles, S);
-    const int per_unit = kWaves / KS, unit_tiles = (tiles + per_unit - 1) / per_unit;
+    const int KS = split<W>(items, tiles, S);
+    const int per_unit = W / KS, unit_tiles = (tiles + per_unit - 1) / per_unit;
     const int rt = wv / KS, ks = wv - rt * KS;
 
     // A wave's place in its stream: tile tt of 16 tokens, super-block sb of a
@@ -345,13 +371,18 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
         const uint64_t base = reinterpret_cast<uint64_t>(w) + ((uint64_t)x.it.expert * M + row0) * S * F::kBlock;
         x.base = base;
         x.rows = min(16, M - row0);
-        const TokenRows<Groups> src(grp, x.it, 0);
+        const auto row_of = [&](int i) {
+            if constexpr (std::is_same<Grp, Groups>::value)
+                return TokenRows<Groups>(grp, x.it, 0).row(i);
+            else
+                return (uint32_t)min(i, grp.tokens - 1);
+        };
         if constexpr (T == 1) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x.off[c] = src.row(4 * c + kg) * (uint32_t)K + 16u * (uint32_t)(r ^ (4 * c + kg));
-            x.woff = src.row(lane >> 1) * (uint32_t)(K >> 3) + 16u * (uint32_t)(lane & 1);
+            for (int c = 0; c < 4; ++c) x.off[c] = row_of(4 * c + kg) * (uint32_t)K + 16u * (uint32_t)(r ^ (4 * c + kg));
+            x.woff = row_of(lane >> 1) * (uint32_t)(K >> 3) + 16u * (uint32_t)(lane & 1);
         } else if (lane < 16 * T) {
-            lds_write<uint32_t>(area + kRows + 4 * lane, src.row(lane));
+            lds_write<uint32_t>(area + kRows + 4 * lane, row_of(lane));
         }
     };
     const auto advance = [&](Pos& x) {
@@ -518,24 +549,40 @@ __global__ __launch_bounds__(kNT, 2 * kHeld) void mmq_group_few_kernel(const uin
     }
 }
 
-template <class F, int T>
-hipError_t launch(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
+template <class F, int T, int W, class Grp>
+hipError_t launch(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Grp& g, int64_t items,
                   const OutEpi& out, hipStream_t stream) {
-    const int64_t units = most_items(g.experts, g.slots, g.lo, g.hi, 16 * T) * ((m + 15) / 16);
-    const dim3 grid((unsigned)std::min<int64_t>(units, 256 * kHeld)), block(kNT);
-    const void* f = (k >> 8) > kFlush ? (const void*)mmq_group_few_kernel<F, T, true>
-                                      : (const void*)mmq_group_few_kernel<F, T, false>;
+    const int64_t units = items * ((m + 15) / 16);
+    const dim3 grid((unsigned)std::min<int64_t>(units, 256 * (16 / W))), block(64 * W);
+    const void* f = (k >> 8) > kFlush ? (const void*)mmq_group_few_kernel<F, T, true, Grp, W>
+                                      : (const void*)mmq_group_few_kernel<F, T, false, Grp, W>;
     void* args[] = {(void*)&w, (void*)&q, (void*)&ds, (void*)&m, (void*)&k, (void*)&out, (void*)&g};
     return hipLaunchKernel(f, grid, block, args, 0, stream);
+}
+
+// Workgroups of 8 waves: with 16, 8 experts of 14336 x 4096 at 2 slots take 73
+// us for 66.  A plain matrix has few units, and 16 waves to share one's k
+// (8192 x 4096 in q6_K, 64 tokens: 28 us for 31).
+template <class F>
+hipError_t grouped(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, const Groups& g,
+                   const OutEpi& out, hipStream_t stream) {
+    const auto items = [&](int64_t tb) { return most_items(g.experts, g.slots, g.lo, g.hi, tb); };
+    return g.hi <= kGroupFewMaxTile ? launch<F, 1, 8>(w, m, k, q, ds, g, items(16), out, stream)
+                                    : launch<F, 4, 8>(w, m, k, q, ds, g, items(64), out, stream);
 }
 
 }  // namespace
 
 hipError_t launch_few_grouped(bool q6k, const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                               const Groups& g, const OutEpi& out, hipStream_t stream) {
-    if (g.hi <= kGroupFewMaxTile)
-        return q6k ? launch<Q6k, 1>(w, m, k, q, ds, g, out, stream) : launch<Q4k, 1>(w, m, k, q, ds, g, out, stream);
-    return q6k ? launch<Q6k, 4>(w, m, k, q, ds, g, out, stream) : launch<Q4k, 4>(w, m, k, q, ds, g, out, stream);
+    return q6k ? grouped<Q6k>(w, m, k, q, ds, g, out, stream) : grouped<Q4k>(w, m, k, q, ds, g, out, stream);
+}
+
+hipError_t launch_q6k_stream(const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds, int n,
+                             const OutEpi& out, hipStream_t stream) {
+    const OneGroup g{n};
+    return n <= 16 ? launch<Q6k, 1, 16>(w, m, k, q, ds, g, 1, out, stream)
+                   : launch<Q6k, 4, 16>(w, m, k, q, ds, g, 1, out, stream);
 }
 
 }  // namespace mmq

@@ -80,6 +80,14 @@ def test_q6k_few_tokens(m, k, n):
     _case(binding.FORMAT_Q6K, m, k, n, n % 5, np.float32, n % 2 == 0, seed=11)
 
 
+@pytest.mark.parametrize("n", [9, 16, 17, 33, 64])
+@pytest.mark.parametrize("m,k", [(4097, 256), (4120, 4352), (8200, 768), (12300, 512)])
+def test_q6k_few_tokens_tall(m, k, n):
+    """Above 4096 rows, where the streaming kernel runs: one to 16 waves on a
+    row tile, and workgroups that go over several units."""
+    _case(binding.FORMAT_Q6K, m, k, n, n % 5, np.float32, n % 2 == 0, seed=13)
+
+
 def test_q6k_few_tokens_long_rows():
     """Beyond 32 super-blocks per wave, where the sums move on."""
     _case(binding.FORMAT_Q6K, 20, 256 * 600, 20, 0, None, False, bias=False, seed=12)

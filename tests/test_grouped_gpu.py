@@ -87,6 +87,22 @@ def test_grouped_small_calls(fmt, counts):
 
 
 @pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+@pytest.mark.parametrize("counts", [[5, 0, 16, 1], [31, 17, 2, 64, 16, 49]], ids=["mean below 16", "mean above 16"])
+@pytest.mark.parametrize("m,k", [(24, 256 * 5), (264, 256 * 17), (2056, 768), (24584, 256)])
+def test_grouped_few_forms(fmt, counts, m, k):
+    """Both forms of the few-token kernel, from units whose k eight waves share
+    to workgroups that go over many units with a wave per row tile."""
+    Case(fmt, counts, m, k, 20, tokens=33).check("few forms")
+
+
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+@pytest.mark.parametrize("count", [3, 20])
+def test_grouped_few_long_rows(fmt, count):
+    """More than 256 super-blocks per wave, where the sums move on."""
+    Case(fmt, [count], 24, 256 * 2100, 21, tokens=4).check("long rows")
+
+
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
 @pytest.mark.parametrize("experts", [63, 64, 65, 130])
 def test_grouped_many_experts(fmt, experts):
     """More experts than a wave has lanes: items are found across the scans."""
