@@ -512,32 +512,26 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
 #pragma unroll
                 for (int j = 0; j < T; ++j)
                     if (T == 1 || tt == j) sum = BIG ? acc2[j] + acc[j] : acc[j];
-                int tile = cur.unit % unit_tiles * per_unit + rt;
-                bool mine = true;
                 if (KS > 1) {
                     red[wv][lane] = sum;
                     lds_barrier();
-                    // wave v < per_unit stores row tile v of the unit
-                    mine = wv < per_unit;
-                    tile += wv - rt;
-                    if (mine) {
-                        sum = red[wv * KS][lane];
-#pragma unroll 1
-                        for (int v = 1; v < KS; ++v) sum += red[wv * KS + v][lane];
-                    }
-                    lds_barrier();
                 }
-                const int row = 16 * tile + r;
-                if (mine && row < M) {
-                    // one store in a loop: four of them fill the registers of
-                    // the main loop with the epilogue's constants
+                // Output i of each lane of a row tile at a time: with KS > 1
+                // spread over the waves.  One store in a loop: unrolled, the
+                // epilogue's constants fill the registers of the main loop.
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = 16 * tt + 4 * kg + i;
-                        if (tok < cur.it.count)
-                            o.put(tok, row, i == 0 ? sum[0] : i == 1 ? sum[1] : i == 2 ? sum[2] : sum[3]);
+                for (int u = KS > 1 ? wv : 0; u < (KS > 1 ? 4 * per_unit : 4); u += KS > 1 ? W : 1) {
+                    const int i = u & 3, tl = KS > 1 ? u >> 2 : rt;
+                    float v = i == 0 ? sum[0] : i == 1 ? sum[1] : i == 2 ? sum[2] : sum[3];
+                    if (KS > 1) {
+                        v = red[tl * KS][lane][i];
+#pragma unroll 1
+                        for (int p = 1; p < KS; ++p) v += red[tl * KS + p][lane][i];
                     }
+                    const int row = 16 * (cur.unit % unit_tiles * per_unit + tl) + r, tok = 16 * tt + 4 * kg + i;
+                    if (row < M && tok < cur.it.count) o.put(tok, row, v);
                 }
+                if (KS > 1) lds_barrier();
             }
 #pragma unroll
             for (int j = 0; j < T; ++j) acc[j] = acc2[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
