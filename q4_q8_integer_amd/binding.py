@@ -735,8 +735,8 @@ def fold_grouped(fmt: int, w: torch.Tensor, experts: int, m: int, k: int, q: tor
         slots = out.shape[0]
     a, out = _epilogue(bias, (experts, m), activation, residual, slots, m, out, f16, q.device)
     _on_one(q.device, w, ds, offsets, rows, bias, residual, out)
-    _run("mmq_fold_grouped", q.device, fmt, w.data_ptr(), experts, m, k, q.data_ptr(), ds.data_ptr(), tokens, _addr(rows), offsets.data_ptr(),
-            slots, a, out.data_ptr())
+    _run("mmq_fold_grouped", q.device, fmt, w.data_ptr(), experts, m, k, q.data_ptr(), ds.data_ptr(), tokens,
+         _addr(rows), offsets.data_ptr(), slots, a, out.data_ptr())
     return out
 
 
@@ -756,8 +756,8 @@ def route(logits: torch.Tensor, top: int, normalize: bool = True, scale: float =
     slot = torch.empty((n, top), dtype=torch.int32, device=dev)
     rows = torch.empty(n * top, dtype=torch.int32, device=dev)
     offsets = (torch.empty if n else torch.zeros)(experts + 1, dtype=torch.int32, device=dev)
-    _run("moe_route", dev, logits.data_ptr(), n, experts, stride, top, normalize, scale, ids.data_ptr(), weights.data_ptr(),
-            slot.data_ptr(), rows.data_ptr(), offsets.data_ptr())
+    _run("moe_route", dev, logits.data_ptr(), n, experts, stride, top, normalize, scale, ids.data_ptr(),
+         weights.data_ptr(), slot.data_ptr(), rows.data_ptr(), offsets.data_ptr())
     return Routing(ids, weights, slot, rows, offsets)
 
 
@@ -780,6 +780,6 @@ def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, residual
             raise ValueError("residual must be [%d, %d], got %s" % (n, m, tuple(residual.shape)))
     out = _out_tensor(out, n, m, torch.float32, y.device)
     _on_one(y.device, slot, weights, residual, out)
-    _run("moe_combine", y.device, y.data_ptr(), y.dtype == torch.float16, slots, m, slot.data_ptr(), weights.data_ptr(), n, top,
-            _addr(residual), out.data_ptr())
+    _run("moe_combine", y.device, y.data_ptr(), y.dtype == torch.float16, slots, m, slot.data_ptr(),
+         weights.data_ptr(), n, top, _addr(residual), out.data_ptr())
     return out

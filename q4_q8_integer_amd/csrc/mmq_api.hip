@@ -384,6 +384,10 @@ int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t
         rc = hip_status(mmq::launch_few_grouped(q6k, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
     if (rc == MMQ_OK && take(q6k ? mmq::kGroupFewMaxQ6k : mmq::kGroupFewMaxQ4k))
         rc = hip_status(mmq::launch_few_grouped(q6k, wb, (int)m, (int)k, q, ds, g, o.epi, stream));
+    // q4_K's binary16 tiles of 64 tokens where the mean is below 96 slots, of 128
+    // above (tiles of 64 / 128, us): 8 experts of 14336 x 4096 with 64 slots each
+    // 159 / 254, 96: 266 / 263, 128: 281 / 274, 256: 518 / 469; 64 experts of 1536
+    // x 4096 with ragged loads of 64 on average 175 / 252, of 96 267 / 271.
     if (rc == MMQ_OK && take(slots)) {
         if (q6k)
             rc = hip_status(mmq::launch_q6k_f16_grouped(wb, (int)m, (int)k, q, ds, g, o.epi, stream));

@@ -17,9 +17,14 @@
 // A workgroup owns a row.  Lane t of it holds the 8-value pieces t, t + T, ..
 // of the row in registers (T threads, V pieces each), so x and y are read
 // once and r, h, q are written once; a DPP quad holds a whole 32-value block,
-// as the quantizer wants it.  Rows beyond kMaxHeld values do not fit the
+// as the quantizer wants it.  Rows beyond 32768 values do not fit the
 // registers: there the workgroup goes over the row in pieces and reads r
 // (or x) again, from cache, for the second norm.
+//
+// Measured: 8192 rows of 4096, y in binary16 with its norm, a gate per channel
+// and h out, 99 us (470 MB: 91 us at the copy rate; HBM bound).  One row of 4096
+// with codes 4 us in a graph, a launch and two reductions across 8 waves; 22 us
+// a call from Python, three allocations among them.
 //
 // With operand tiles a lane's codes are one 16-byte slot, and the slots of
 // consecutive tokens are adjacent: eight consecutive rows go to the same XCD
