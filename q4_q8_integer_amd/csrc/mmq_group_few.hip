@@ -30,18 +30,19 @@
 //     also from one unit to the next.  One area per wave leaves room for 16
 //     waves per CU: with 8 waves and two areas a SIMD's two waves issued
 //     vector instructions at less than half its rate (8 experts of 14336 x
-//     4096, 8 slots each: 99 us, 87 of them without any copies; this form 77).
+//     4096, 8 slots each: 99 us, 87 of them without any copies; this form 71).
 //   * T = 1 takes items of up to 16 tokens.  T = 4 takes up to 64, the weights
 //     decoded once for all their tiles; its copy addresses are computed anew,
 //     which leaves the loop its registers.
 //
-// Measured (graph of calls): q4_K, 14336 x 4096, 2 / 8 experts of 2 slots 21 /
-// 66-71 us (weights alone at the copy rate 13 / 52), 8 of 16 86, of 32 125; 64
-// experts of 1536 x 4096 at 2 / 16 / 32 slots 58 / 76 / 111 us (44 / 46 / 48);
-// q6_K, 64 of 4096 x 1536 at 1 / 16 / 32 / 64 slots 94 / 106 / 161 / 267 us (64 /
-// 68 / 71 / 79).  Up to 16 slots the weights stream at 3 to 4 TB/s; above, vector
-// issue bounds it (per 16 x 16 outputs and chunk 8 operations in q4_K, 16 in
-// q6_K, and the decode).
+// Measured (graph of calls): q4_K, 14336 x 4096, 2 / 8 experts of 2 slots 20 /
+// 64-70 us (weights alone at the copy rate 13 / 52), 8 of 16 83, of 32 120; 64
+// experts of 1536 x 4096 at 2 / 16 / 32 slots 56 / 73 / 105 us (44 / 46 / 48);
+// q6_K, 64 of 4096 x 1536 at 1 / 16 / 32 / 64 slots 90 / 104 / 162 / 270 us (64 /
+// 68 / 71 / 79).  Up to 16 slots the weights stream at 3 to 4.2 TB/s (with the
+// codes of 4 tokens only and two steps in flight no faster, so not for want of
+// copies in flight); above, vector issue bounds it (per 16 x 16 outputs and
+// chunk 8 operations in q4_K, 16 in q6_K, and the decode).
 #include <algorithm>
 #include <type_traits>
 
@@ -89,33 +90,51 @@ __device__ __forceinline__ void lds_barrier() {
 struct OneGroup {
     int tokens;
 };
-template <int TB>
-__device__ __forceinline__ Item find_item(const OneGroup& g, int i) {
-    return Item{0, 0, g.tokens, i == 0};
-}
-template <int TB>
-__device__ __forceinline__ int count_items(const OneGroup&) {
-    return 1;
-}
 
-// The number of items of a launch (wave-collective).
-template <int TB>
-__device__ __forceinline__ int count_items(const Groups& g) {
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    for (int base = 0; base < g.experts; base += 64) {
-        const int e = base + lane;
-        int c = 0;
-        if (e < g.experts) {
-            const int a = min(max(g.offsets[e], 0), g.slots);
-            c = min(max(g.offsets[e + 1], a), g.slots) - a;
-        }
-        n += c >= g.lo && c <= g.hi ? (c + TB - 1) / TB : 0;
-    }
+// The items of a launch: their number and item i (wave-collective).  Up to 64
+// experts are held in registers, lane e the slots of expert e, so that only
+// the kernel's start loads the offsets.
+template <int TB, class Grp>
+struct Finder {
+    const Groups& g;
+    int first, slots, incl;   // first slot, slots, items up to this expert
+    int total;
+    __device__ __forceinline__ explicit Finder(const Groups& grp) : g(grp), total(0) {
+        const int lane = threadIdx.x & 63;
+        for (int base = 0; base < g.experts; base += 64) {
+            const int e = base + lane;
+            first = slots = 0;
+            if (e < g.experts) {
+                first = min(max(g.offsets[e], 0), g.slots);
+                slots = min(max(g.offsets[e + 1], first), g.slots) - first;
+            }
+            incl = slots >= g.lo && slots <= g.hi ? (slots + TB - 1) / TB : 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    return __builtin_amdgcn_readfirstlane(n);
-}
+            for (int o = 1; o < 64; o <<= 1) {
+                const int up = __shfl_up(incl, o);
+                if (lane >= o) incl += up;
+            }
+            total += __builtin_amdgcn_readlane(incl, 63);
+        }
+    }
+    __device__ __forceinline__ int count() const { return total; }
+    __device__ __forceinline__ Item operator()(int i) const {
+        if (g.experts > 64) return find_item<TB>(g, i);
+        const uint64_t past = __ballot(incl > i);
+        if (!past) return Item{0, 0, 0, false};
+        const int l = __builtin_ctzll(past);
+        const int before = l ? __builtin_amdgcn_readlane(incl, l - 1) : 0;
+        const int skip = (i - before) * TB, n = __builtin_amdgcn_readlane(slots, l);
+        return Item{l, __builtin_amdgcn_readlane(first, l) + skip, min(TB, n - skip), true};
+    }
+};
+template <int TB>
+struct Finder<TB, OneGroup> {
+    const int tokens;
+    __device__ __forceinline__ explicit Finder(const OneGroup& g) : tokens(g.tokens) {}
+    __device__ __forceinline__ int count() const { return 1; }
+    __device__ __forceinline__ Item operator()(int i) const { return Item{0, 0, tokens, i == 0}; }
+};
 
 // ------------------------------------------------------------------- q4_K
 struct Q4k {
@@ -344,7 +363,8 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
     const int tiles = (M + 15) >> 4;
     const uint32_t area = (uint32_t)(uintptr_t)(Lds)areas + (uint32_t)(wv * kArea);
 
-    const int items = count_items<16 * T>(grp);
+    const Finder<16 * T, Grp> find(grp);
+    const int items = find.count();
     const int KS = split<W>(items, tiles, S);
     const int per_unit = W / KS, unit_tiles = (tiles + per_unit - 1) / per_unit;
     const int rt = wv / KS, ks = wv - rt * KS;
@@ -364,7 +384,7 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
         x.sb = ks;
         x.tt = 0;
         const int item = unit / unit_tiles, ut = unit - item * unit_tiles;
-        x.it = find_item<16 * T>(grp, item);
+        x.it = find(item);
         if (!x.it.valid) return;
         // past the last tile: its rows again, not stored
         const int row0 = min(ut * per_unit + rt, tiles - 1) * 16;
