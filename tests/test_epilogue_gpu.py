@@ -161,6 +161,54 @@ def test_epilogue_row_split_launch():
     _case(binding.FORMAT_Q4K, 11008, 256, 512, binding.ACT_RELU, np.float32, False)
 
 
+def test_epilogue_keeps_nan_and_infinities_of_the_residual():
+    """ReLU of NaN is NaN; the residual is added as it is."""
+    m, k, n = 64, 256, 20
+    w, q, ds = _setup(binding.FORMAT_Q4K, 31, m, k, n)
+    b = np.zeros(m, np.float32)
+    b[3], b[5], b[7] = np.nan, np.inf, -np.inf
+    r = np.zeros((n, m), np.float32)
+    r[:, 9], r[:, 11] = np.inf, np.nan
+    note("epilogue nan")
+    out = binding.fold_epilogue(binding.FORMAT_Q4K, w, m, k, q, ds, to_dev(b), binding.ACT_RELU, to_dev(r))
+    torch.cuda.synchronize()
+    out = out.cpu().numpy()
+    assert np.isnan(out[:, 3]).all() and (out[:, 5] == np.inf).all() and (out[:, 7] == 0).all()
+    assert (out[:, 9] == np.inf).all() and np.isnan(out[:, 11]).all()
+    keep = [c for c in range(m) if c not in (3, 5, 7, 9, 11)]
+    assert np.isfinite(out[:, keep]).all()
+
+
+@pytest.mark.parametrize("fmt,m,n", [(binding.FORMAT_Q4K, 300, 3), (binding.FORMAT_Q4K, 300, 200),
+                                     (binding.FORMAT_Q6K, 300, 30), (binding.FORMAT_Q6K, 4200, 30),
+                                     (binding.FORMAT_Q6K, 300, 100)])
+def test_epilogue_on_two_streams_and_in_a_graph(fmt, m, n):
+    k = 1024
+    w, q, ds = _setup(fmt, 32, m, k, n)
+    bias = torch.randn(m, device=w.device)
+    x = torch.randn(n, m, device=w.device)
+    call = lambda out: binding.fold_epilogue(fmt, w, m, k, q, ds, bias, binding.ACT_GELU, x, out=out)
+    note("epilogue streams fmt=%d m=%d n=%d" % (fmt, m, n))
+    ref, out = call(None), torch.zeros(n, m, device=w.device)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            a = call(None)
+        b = call(None)
+        torch.cuda.synchronize()
+        assert torch.equal(a, ref) and torch.equal(b, ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out)
+    for i in range(4):
+        x.copy_(torch.randn(n, m, device=w.device))
+        g.replay()
+        eager = call(None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), i
+
+
 def test_epilogue_binding_refusals():
     m, k, n = 32, 256, 4
     w, q, ds = _setup(binding.FORMAT_Q4K, 1, m, k, n)
