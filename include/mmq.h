@@ -358,9 +358,9 @@ int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n);
  * where fold is the float32 result of the entry point of `format` for the
  * same arguments, bit for bit (with every operand absent and MMQ_ACT_NONE the
  * call is that entry point), except MMQ_FORMAT_Q6K at 9 to 64 tokens, which
- * runs a kernel of its own with the same accuracy.  Outputs and residuals may be rows of larger
- * arrays (strides), and the residual may be the output itself (same type and
- * stride: x += W h); otherwise they must not overlap.
+ * runs kernels of its own with the same accuracy.  Outputs and residuals may be
+ * rows of larger arrays (strides), and the residual may be the output itself
+ * (same type and stride: x += W h); otherwise they must not overlap.
  *
  *   w, q, ds : as for the entry point of `format` (q: its int8 codes or its
  *              operand tiles); m, k, n and their limits too.
@@ -417,7 +417,9 @@ int mmq_fold_epilogue(int format, const void *w, int64_t m, int64_t k, const voi
  * A value of rows or offsets outside its range is clamped into it (the result
  * is then meaningless, but nothing outside the arrays is touched).  The
  * float32 arithmetic is that of the fold entry points on the kernel that the
- * group's size takes, with the same accuracy.  Limits: experts <= 4096,
+ * group's size takes, with the same accuracy; equal calls give equal bits, but
+ * the order of a sum, and so a result's last bits, may depend on the sizes of
+ * all groups.  Limits: experts <= 4096,
  * tokens*k < 2^32, slots*m and experts*m*(k/256)*(block bytes) below 2^40.
  * slots or m of 0 is an empty call.
  */
