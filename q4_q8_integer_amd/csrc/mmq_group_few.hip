@@ -317,24 +317,26 @@ struct Q6k {
     }
 };
 
-// The waves on a row tile: the least time by a model of the work on the
-// busiest CU, its units times a unit's steps and 4/3 of a step for its ends,
-// a quarter more where a CU has one workgroup of 8 waves.  (q4_K, k = 4096,
-// KS = 1 / 2 / 4 / 8: 1792 tiles 21.7 / 20.2 / 21.5 / 21.8 us, 2688 tiles 31.1 /
-// 24.6 / 28.5 us, 7168 tiles 82.5 / 71.8 us.)
+// The waves on a row tile, as the logarithm of their number: the least time by
+// a model of the work on the busiest CU, its units times a unit's steps and
+// 4/3 of a step for its ends, a quarter more where a CU has one workgroup of 8
+// waves.  (q4_K, k = 4096, KS = 1 / 2 / 4 / 8: 1792 tiles 21.7 / 20.2 / 21.5 /
+// 21.8 us, 2688 tiles 31.1 / 24.6 / - / 28.5 us, 7168 tiles 82.5 / - / - / 71.8 us.)
+// With 2^16 tiles or more (32 units per CU) a wave each; below that the model's
+// numbers fit 32 bits, as S <= 2^16.
 template <int W>
 __device__ __forceinline__ int split(int items, int tiles, int S) {
-    int best = 1;
-    uint64_t least = ~0ull;
+    if ((uint64_t)(uint32_t)items * (uint32_t)tiles >= 1u << 16) return 0;
+    int best = 0;
+    uint32_t least = ~0u;
 #pragma unroll
     for (int l = 0; 1 << l <= W; ++l) {
-        const uint32_t groups = ((tiles << l) + W - 1) / W;   // units of an item
-        const uint64_t units = (uint64_t)(uint32_t)items * groups;
-        const uint64_t cost =
-            ((units + 255) >> 8) * (uint32_t)(3 * ((S + (1 << l) - 1) >> l) + 4) * (W < 16 && units <= 256 ? 5u : 4u);
+        const uint32_t units = (uint32_t)items * ((uint32_t)((tiles << l) + W - 1) / W);
+        const uint32_t cost = ((units + 255) >> 8) * (uint32_t)(3 * ((S + (1 << l) - 1) >> l) + 4) *
+                              (W < 16 && units <= 256 ? 5u : 4u);
         if ((1 << l) <= S && cost < least) {
             least = cost;
-            best = 1 << l;
+            best = l;
         }
     }
     return best;
@@ -365,15 +367,17 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
 
     const Finder<16 * T, Grp> find(grp);
     const int items = find.count();
-    const int KS = split<W>(items, tiles, S);
-    const int per_unit = W / KS, unit_tiles = (tiles + per_unit - 1) / per_unit;
-    const int rt = wv / KS, ks = wv - rt * KS;
+    // KS = 1 << ksl waves on a row tile, a unit's row tiles, its place among an
+    // item's (units are numbered item by item)
+    const int ksl = split<W>(items, tiles, S), KS = 1 << ksl;
+    const int per_unit = W >> ksl, unit_tiles = (int)((uint32_t)((tiles << ksl) + W - 1) / W);
+    const int rt = wv >> ksl, ks = wv & (KS - 1);
 
     // A wave's place in its stream: tile tt of 16 tokens, super-block sb of a
     // row tile (its rows from base) of a unit; off, woff (T = 1): this lane's
     // copy offsets of the item's tokens' codes and words at super-block 0.
     struct Pos {
-        int unit, sb, tt;
+        int unit, tile0, sb, tt;   // tile0: the unit's first row tile
         Item it;
         uint64_t base;
         int rows;
@@ -383,11 +387,12 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
         x.unit = unit;
         x.sb = ks;
         x.tt = 0;
-        const int item = unit / unit_tiles, ut = unit - item * unit_tiles;
+        const int item = (int)((uint32_t)unit / (uint32_t)unit_tiles);
+        x.tile0 = (unit - item * unit_tiles) * per_unit;
         x.it = find(item);
         if (!x.it.valid) return;
         // past the last tile: its rows again, not stored
-        const int row0 = min(ut * per_unit + rt, tiles - 1) * 16;
+        const int row0 = min(x.tile0 + rt, tiles - 1) * 16;
         const uint64_t base = reinterpret_cast<uint64_t>(w) + ((uint64_t)x.it.expert * M + row0) * S * F::kBlock;
         x.base = base;
         x.rows = min(16, M - row0);
@@ -548,7 +553,7 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
 #pragma unroll 1
                         for (int p = 1; p < KS; ++p) v += red[tl * KS + p][lane][i];
                     }
-                    const int row = 16 * (cur.unit % unit_tiles * per_unit + tl) + r, tok = 16 * tt + 4 * kg + i;
+                    const int row = 16 * (cur.tile0 + tl) + r, tok = 16 * tt + 4 * kg + i;
                     if (row < M && tok < cur.it.count) o.put(tok, row, v);
                 }
                 if (KS > 1) lds_barrier();
