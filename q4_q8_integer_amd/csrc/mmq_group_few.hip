@@ -91,6 +91,19 @@ struct OneGroup {
     int tokens;
 };
 
+// The sum of v over this lane and those below it: DPP moves within rows of 16
+// lanes (row_shr 1, 2, 4, 8), then from lane 15 of a row to the next row and
+// from lane 31 to the upper half (row_bcast 15, 31).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
 // The items of a launch: their number and item i (wave-collective).  Up to 64
 // experts are held in registers, lane e the slots of expert e, so that only
 // the kernel's start loads the offsets.
@@ -108,12 +121,7 @@ struct Finder {
                 first = min(max(g.offsets[e], 0), g.slots);
                 slots = min(max(g.offsets[e + 1], first), g.slots) - first;
             }
-            incl = slots >= g.lo && slots <= g.hi ? (slots + TB - 1) / TB : 0;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int up = __shfl_up(incl, o);
-                if (lane >= o) incl += up;
-            }
+            incl = wave_scan(slots >= g.lo && slots <= g.hi ? (slots + TB - 1) / TB : 0);
             total += __builtin_amdgcn_readlane(incl, 63);
         }
     }
