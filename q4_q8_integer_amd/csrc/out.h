@@ -12,9 +12,10 @@
 // run-time values: per output they cost a few scalar branches in kernels
 // that spend k / 32 vector operations on it, where a template per choice
 // would multiply every kernel by 40.  Measured: 4096 x 4096, 2630 tokens, fold
-// 168-172 us, with bias and float32 residual 176 (the residual's 43 MB are 8 us
-// at the copy rate), with bias and SiLU 184, GELU 187 (the consumer waves'
-// last step); 28672 x 8192, 7 tokens, 31 us with any of them, as the fold.
+// 161-170 us, with bias and float32 residual 172 (the residual's 43 MB are 8 us
+// at the copy rate), with bias and SiLU 170 (184 with an exponential and a
+// division of full range), GELU 180 (the consumer waves' last step); 28672 x
+// 8192, 7 tokens, 30-31 us with any of them, as the fold.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -48,21 +49,24 @@ struct OutF16 {
 
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-// x * sigmoid(x); for x below -88 the exponential overflows and the result
-// is -0, as the exact value (below 1e-36) is to 36 digits.
-__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
+// v * sigmoid(x) = v / (1 + exp(-x)) on the hardware's exponential and
+// reciprocal (one ulp each), five instructions.  The product with log2(e) is
+// rounded once, which moves the result as a rounding of x does: by |x| 2^-24
+// of it in the lower tail, less above.  Below x = -88 the exponential
+// overflows and the result is -0, as the exact value (below 1e-36) is to 36
+// digits.
+__device__ __forceinline__ float times_sigmoid(float v, float x) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
+}
 
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case kActRelu: return v < 0.0f ? 0.0f : v;   // NaN stays
-        case kActSilu: return silu(v);
+        case kActSilu: return times_sigmoid(v, v);
         // v * Phi(v); erfc keeps its relative accuracy where 1 + erf cancels
         case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
         // 0.5 v (1 + tanh u) = v * sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3)
-        case kActGeluTanh: {
-            const float u2 = 1.59576912160573076f * fmaf(0.044715f * v * v, v, v);
-            return v / (1.0f + expf(-u2));
-        }
+        case kActGeluTanh: return times_sigmoid(v, 1.59576912160573076f * fmaf(0.044715f * v * v, v, v));
         default: return v;
     }
 }
