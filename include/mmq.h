@@ -350,8 +350,8 @@ int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n);
 
 /*
  * mmq_fold_epilogue - a fold entry point with an epilogue: what follows the
- * matmul elementwise is done as its results are stored, in float32, with one
- * rounding at a binary16 store.
+ * matmul elementwise is done as its results are stored, in float32 (exp and the
+ * sigmoid's reciprocal to an ulp), with one rounding at a binary16 store.
  *
  *   out[t][o] = act( fold[t][o] + bias[o] ) + residual[t][o]
  *
