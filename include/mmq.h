@@ -357,8 +357,9 @@ int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n);
  *
  * where fold is the float32 result of the entry point of `format` for the
  * same arguments, bit for bit (with every operand absent and MMQ_ACT_NONE the
- * call is that entry point), except MMQ_FORMAT_Q6K at 9 to 64 tokens, which
- * runs kernels of its own with the same accuracy.  Outputs and residuals may be
+ * call is that entry point), except MMQ_FORMAT_Q6K at 9 to 64 tokens, and above
+ * while ceil(m/16)*ceil(n/64) <= 1536 (and n*k < 2^32), which runs kernels of its own with the
+ * same accuracy.  Outputs and residuals may be
  * rows of larger arrays (strides), and the residual may be the output itself
  * (same type and stride: x += W h); otherwise they must not overlap.
  *

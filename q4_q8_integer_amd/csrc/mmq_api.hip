@@ -237,6 +237,19 @@ int q6k_fold_launcher(int kernel, int64_t m, int64_t n, FoldLaunch* f) {
     }
 }
 
+// Where a q6_K call with an epilogue runs kernels of its own (launch_q6k_few,
+// launch_q6k_stream): from 9 tokens, while there are few tiles of 16 rows x 64
+// tokens for the binary16 kernel's 128 x 128 ones to fill the chip.  Streaming
+// against binary16, us: 4096 x 11008 at 128 / 256 / 512 tokens (512 / 1024 /
+// 2048 tiles) 62 / 113 / 204 and 235 / 228 / 223; 4096 x 4096 at 128 / 384 / 512
+// (512 / 1536 / 2048) 28 / 78 / 84 and 81 / 78 / 78; 8192 x 4096 at 128 / 192 /
+// 320 (1024 / 1536 / 2560) 46 / 78 / 120 and 81 / 79 / 79.
+// Their offsets into q are 32 bits.
+bool q6k_epilogue_own(int64_t m, int64_t k, int64_t n) {
+    return n > mmq::kQ6kGemvMaxN &&
+           (n <= mmq::kQ6kFewMaxN || ((m + 15) / 16 * ((n + 63) / 64) <= 1536 && n * k < (1LL << 32)));
+}
+
 int q6k_fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const uint32_t* ds,
                    int64_t n, const mmq::Out& out, int kernel, hipStream_t stream) {
     bool empty = false;
@@ -244,12 +257,12 @@ int q6k_fold_entry(const void* w, int64_t m, int64_t k, const int8_t* q, const u
     if (rc != MMQ_OK || empty) return rc;
     if (!ds) return MMQ_ERR_NULL;
     if (!aligned16(ds)) return MMQ_ERR_ALIGN;
-    if (out.kind == mmq::kOutEpi && n > mmq::kQ6kGemvMaxN && n <= mmq::kQ6kFewMaxN) {
+    if (out.kind == mmq::kOutEpi && q6k_epilogue_own(m, k, n)) {
         if (!threads_ok((m + 15) / 16, 512)) return MMQ_ERR_OVERFLOW;
         rc = check_device();
         if (rc != MMQ_OK) return rc;
-        const auto few = m > mmq::kQ6kFewMaxM ? mmq::launch_q6k_stream : mmq::launch_q6k_few;
-        return hip_status(few(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out.epi, stream));
+        const auto own = m <= mmq::kQ6kFewMaxM && n <= mmq::kQ6kFewMaxN ? mmq::launch_q6k_few : mmq::launch_q6k_stream;
+        return hip_status(own(static_cast<const uint8_t*>(w), (int)m, (int)k, q, ds, (int)n, out.epi, stream));
     }
     FoldLaunch launch = nullptr;
     rc = q6k_fold_launcher(kernel, m, n, &launch);

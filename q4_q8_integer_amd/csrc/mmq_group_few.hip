@@ -1,6 +1,6 @@
 // mmq_group_few.hip - streaming few-token products on 16x16x32 int8 MFMA: the
 // matmuls grouped by expert for experts of few slots, and q6_K with an
-// epilogue for few tokens on tall matrices.
+// epilogue where there are few tiles of tokens and rows.
 //
 // Method as in the other kernels: exact integer dots of a chunk (k = 32; in
 // q6_K of its two scale groups, k = 16), then the fold.
@@ -86,7 +86,7 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// One item of `tokens` tokens, the rows of q.
+// A plain call: `tokens` tokens, the rows of q.
 struct OneGroup {
     int tokens;
 };
@@ -140,8 +140,10 @@ template <int TB>
 struct Finder<TB, OneGroup> {
     const int tokens;
     __device__ __forceinline__ explicit Finder(const OneGroup& g) : tokens(g.tokens) {}
-    __device__ __forceinline__ int count() const { return 1; }
-    __device__ __forceinline__ Item operator()(int i) const { return Item{0, 0, tokens, i == 0}; }
+    __device__ __forceinline__ int count() const { return (tokens + TB - 1) / TB; }
+    __device__ __forceinline__ Item operator()(int i) const {
+        return Item{0, i * TB, min(TB, tokens - i * TB), i < count()};
+    }
 };
 
 // ------------------------------------------------------------------- q4_K
@@ -408,7 +410,7 @@ __global__ __launch_bounds__(64 * W, 4) void mmq_group_few_kernel(const uint8_t*
             if constexpr (std::is_same<Grp, Groups>::value)
                 return TokenRows<Groups>(grp, x.it, 0).row(i);
             else
-                return (uint32_t)min(i, grp.tokens - 1);
+                return (uint32_t)(x.it.start + min(i, x.it.count - 1));
         };
         if constexpr (T == 1) {
 #pragma unroll
@@ -609,7 +611,7 @@ hipError_t launch_q6k_stream(const uint8_t* w, int m, int k, const int8_t* q, co
                              const OutEpi& out, hipStream_t stream) {
     const OneGroup g{n};
     return n <= 16 ? launch<Q6k, 1, 16>(w, m, k, q, ds, g, 1, out, stream)
-                   : launch<Q6k, 4, 16>(w, m, k, q, ds, g, 1, out, stream);
+                   : launch<Q6k, 4, 16>(w, m, k, q, ds, g, (n + 63) / 64, out, stream);
 }
 
 }  // namespace mmq

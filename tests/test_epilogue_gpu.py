@@ -38,6 +38,11 @@ def _setup(fmt, seed, m, k, n):
     return w, q, ds
 
 
+def _own(fmt, m, n):
+    """Whether the call runs a kernel that the fold entry point does not."""
+    return fmt == binding.FORMAT_Q6K and n > 8 and (n <= 64 or -(-m // 16) * -(-n // 64) <= 1536)
+
+
 def _case(fmt, m, k, n, act, residual, f16, bias=True, seed=0):
     note("epilogue fmt=%d m=%d k=%d n=%d act=%d residual=%s f16=%s" % (fmt, m, k, n, act, residual, f16))
     w, q, ds = _setup(fmt, seed + n, m, k, n)
@@ -49,7 +54,7 @@ def _case(fmt, m, k, n, act, residual, f16, bias=True, seed=0):
     out = binding.fold_epilogue(fmt, w, m, k, q, ds, None if b is None else to_dev(b), act,
                                 None if r is None else to_dev(r), f16=f16)
     torch.cuda.synchronize()
-    if fmt == binding.FORMAT_Q6K and 9 <= n <= 64:
+    if _own(fmt, m, n):
         # a kernel of its own: its fold is held to the oracle, and the epilogue to its fold
         fold = binding.fold_epilogue(fmt, w, m, k, q, ds)
         torch.cuda.synchronize()
@@ -78,6 +83,22 @@ def test_q6k_few_tokens(m, k, n):
     inside 16 rows and inside a 16-byte piece, one super-block (seven idle
     waves), a whole round of the waves, one more, and 65."""
     _case(binding.FORMAT_Q6K, m, k, n, n % 5, np.float32, n % 2 == 0, seed=11)
+
+
+@pytest.mark.parametrize("n", [65, 128, 129, 200, 300])
+@pytest.mark.parametrize("m,k", [(1, 256), (37, 2048), (260, 4352), (1030, 768)])
+def test_q6k_more_tokens_on_small_matrices(m, k, n):
+    """Above 64 tokens the streaming kernel takes several items of 64."""
+    assert _own(binding.FORMAT_Q6K, m, n)
+    _case(binding.FORMAT_Q6K, m, k, n, n % 5, np.float16 if m % 4 else np.float32, n % 2 == 0, seed=14)
+
+
+@pytest.mark.parametrize("act", [0, 2, 3])
+@pytest.mark.parametrize("m,n", [(16404, 129), (33000, 65), (16401, 130)])
+def test_q6k_binary16_kernel(m, n, act):
+    """Enough tiles for the binary16 kernel: the fold entry point's bits."""
+    assert not _own(binding.FORMAT_Q6K, m, n)
+    _case(binding.FORMAT_Q6K, m, 512, n, act, np.float32, act == 2, seed=15)
 
 
 @pytest.mark.parametrize("n", [9, 16, 17, 33, 64])
@@ -142,7 +163,7 @@ def test_strided_outputs_in_place_residual(fmt, n, m, pad):
     columns beside it are left as they were."""
     k = 512
     w, q, ds = _setup(fmt, 7, m, k, n)
-    fold = _plain(fmt, w, m, k, q, ds).cpu().numpy()
+    fold = (binding.fold_epilogue if _own(fmt, m, n) else _plain)(fmt, w, m, k, q, ds).cpu().numpy()
     rng = np.random.default_rng(9)
     r = rng.standard_normal((n, m)).astype(np.float32)
     wide = torch.full((n, m + pad), 5.0, device="cuda:0")

@@ -85,6 +85,23 @@ def test_epilogue_output_past_2_31_values():
     _same_rows(out, small, idx, "epilogue")
 
 
+def test_epilogue_q6k_past_4_gib_of_codes():
+    """A small matrix on so many long rows that their codes pass 4 GiB: the
+    binary16 kernel, with the fold entry point's bits."""
+    m, k, n, pool = 16, 65792, 65536, 64
+    assert n * k > 2 ** 32
+    note("large q6_K epilogue")
+    w = to_dev(refs.weights("q6k", 71, m, k).reshape(-1))
+    q, ds = oracle.quantize(synth.random_activations(6, pool, k, "outliers"))
+    idx = torch.randint(0, pool, (n,), device=DEV)
+    dq, dds = to_dev(q)[idx].contiguous(), to_dev(ds.view(np.int32))[idx].contiguous()
+    out, fold = binding.fold_epilogue(binding.FORMAT_Q6K, w, m, k, dq, dds), binding.q6k_fp32(w, m, k, dq, dds)
+    torch.cuda.synchronize()
+    assert torch.equal(out, fold)
+    check_fp32(out[-200:].cpu().numpy(), refs.fold64("q6k", w.cpu().numpy().reshape(m, -1), m, k, q, ds)[idx[-200:].cpu()],
+               "last rows")
+
+
 def test_norm_past_2_31_values():
     k, n, pool = 4128, (1 << 19) + 3, 64
     assert n * k > 2 ** 31
