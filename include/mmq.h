@@ -415,13 +415,14 @@ int mmq_fold_epilogue(int format, const void *w, int64_t m, int64_t k, const voi
  *   offsets : int32 [experts + 1], not decreasing, within 0 .. slots.
  *   slots   : rows of out (and of the residual): the most there can be.
  *   epilogue, out : as for mmq_fold_epilogue; bias is [experts][m].
- * A value of rows or offsets outside its range is clamped into it (the result
- * is then meaningless, but nothing outside the arrays is touched).  The
- * float32 arithmetic is that of the fold entry points on the kernel that the
- * group's size takes, with the same accuracy; equal calls give equal bits, but
- * the order of a sum, and so a result's last bits, may depend on the sizes of
- * all groups.  Limits: experts <= 4096,
- * tokens*k < 2^32, slots*m and experts*m*(k/256)*(block bytes) below 2^40.
+ * A value of rows or offsets outside its range is clamped into it, and an
+ * offset below an earlier one counts as the largest before it (the result is
+ * then meaningless, but nothing outside the arrays is touched).  The float32
+ * arithmetic is that of the fold entry points on the kernel that the group's
+ * size takes, with the same accuracy; equal calls give equal bits, but the
+ * order of a sum, and so a result's last bits, may depend on the sizes of all
+ * groups.  Limits: experts <= 4096, tokens*k < 2^32, slots*m and
+ * experts*m*(k/256)*(block bytes) below 2^40.
  * slots or m of 0 is an empty call.
  */
 int mmq_fold_grouped(int format, const void *w, int64_t experts, int64_t m, int64_t k, const int8_t *q,

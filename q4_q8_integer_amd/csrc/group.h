@@ -9,8 +9,10 @@
 // strides of the grid until there are no more, so a launch whose experts
 // are all outside [lo, hi] costs one lookup per workgroup.
 //
-// Offsets and rows outside their ranges are clamped: a wrong one gives wrong
-// values, never an access outside the buffers.
+// Offsets and rows outside their ranges are clamped, and an offset below an
+// earlier one counts as the largest before it: a wrong one gives wrong values,
+// never an access outside the buffers.  So the groups never overlap, and a
+// launch has no more items than the slots make (most_items).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -36,20 +38,51 @@ struct Item {
     bool valid;
 };
 
+// The largest v of this lane and those below it: DPP moves within rows of 16
+// lanes (row_shr 1, 2, 4, 8), then from lane 15 of a row to the next row and
+// from lane 31 to the upper half (row_bcast 15, 31); a lane without a source
+// keeps its own.
+__device__ __forceinline__ int wave_max_scan(int v) {
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x111, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x112, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x114, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x118, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x142, 0xA, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xC, 0xF, false));
+    return v;
+}
+
+// The slots of expert base + lane.  high: the largest offset before this
+// chunk of 64 experts, and then before the next (0 for the first); offsets
+// that do not decrease need no scan for it.  Wave-collective, every lane
+// active.
+struct Span {
+    int first, slots;
+};
+__device__ __forceinline__ Span expert_slots(const Groups& g, int base, int& high) {
+    const int e = base + (int)(threadIdx.x & 63);
+    int a = high, b = high;
+    if (e < g.experts) {
+        a = min(max(g.offsets[e], 0), g.slots);
+        b = min(max(g.offsets[e + 1], 0), g.slots);
+    }
+    if (__ballot(b < a || a < high)) {
+        a = max(wave_max_scan(a), high);
+        b = max(a, b);
+    }
+    high = __builtin_amdgcn_readlane(b, 63);
+    return Span{a, b - a};
+}
+
 // Item i of the launch.  Wave-collective, every lane active; the result is
 // wave-uniform.
 template <int TB>
 __device__ __forceinline__ Item find_item(const Groups& g, int i) {
     const int lane = threadIdx.x & 63;
-    int before = 0;
+    int before = 0, high = 0;
     for (int base = 0; base < g.experts; base += 64) {
-        const int e = base + lane;
-        int a = 0, c = 0;
-        if (e < g.experts) {
-            a = min(max(g.offsets[e], 0), g.slots);
-            c = min(max(g.offsets[e + 1], a), g.slots) - a;
-        }
-        const int items = c >= g.lo && c <= g.hi ? (c + TB - 1) / TB : 0;
+        const Span s = expert_slots(g, base, high);
+        const int items = s.slots >= g.lo && s.slots <= g.hi ? (s.slots - 1) / TB + 1 : 0;   // lo >= 1
         int incl = items;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -60,8 +93,8 @@ __device__ __forceinline__ Item find_item(const Groups& g, int i) {
         if (past) {
             const int l = __builtin_ctzll(past);
             const int skip = (i - before - __builtin_amdgcn_readlane(incl - items, l)) * TB;
-            const int cl = __builtin_amdgcn_readlane(c, l);
-            return Item{base + l, __builtin_amdgcn_readlane(a, l) + skip, min(TB, cl - skip), true};
+            const int n = __builtin_amdgcn_readlane(s.slots, l);
+            return Item{base + l, __builtin_amdgcn_readlane(s.first, l) + skip, min(TB, n - skip), true};
         }
         before += __builtin_amdgcn_readlane(incl, 63);
     }

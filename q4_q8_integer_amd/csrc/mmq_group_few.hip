@@ -113,14 +113,11 @@ struct Finder {
     int first, slots, incl;   // first slot, slots, items up to this expert
     int total;
     __device__ __forceinline__ explicit Finder(const Groups& grp) : g(grp), total(0) {
-        const int lane = threadIdx.x & 63;
+        int high = 0;
         for (int base = 0; base < g.experts; base += 64) {
-            const int e = base + lane;
-            first = slots = 0;
-            if (e < g.experts) {
-                first = min(max(g.offsets[e], 0), g.slots);
-                slots = min(max(g.offsets[e + 1], first), g.slots) - first;
-            }
+            const Span s = expert_slots(g, base, high);
+            first = s.first;
+            slots = s.slots;
             incl = wave_scan(slots >= g.lo && slots <= g.hi ? (slots + TB - 1) / TB : 0);
             total += __builtin_amdgcn_readlane(incl, 63);
         }
