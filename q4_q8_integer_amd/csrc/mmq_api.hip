@@ -377,8 +377,13 @@ int grouped_entry(int format, const void* w, int64_t experts, int64_t m, int64_t
         !aligned16(out))
         return MMQ_ERR_ALIGN;
     if (experts > 1 && (m * (k / 256) * block) % 16 != 0) return MMQ_ERR_ALIGN;   // every expert's first row
-    // tiles are numbered in 32 bits; one slot per item and 16 rows per tile is the most there can be
-    if (mmq::most_items(experts, slots, 1, slots, 1) * ((m + 15) / 16) > kMaxDim) return MMQ_ERR_OVERFLOW;
+    // The kernels number their tiles (items times tiles of rows) in 32 bits, which
+    // hold the most that the limits above leave.  An item of the four-tile few-token
+    // form takes 64 slots, all but the last of an expert, and 16 rows: at most
+    // slots*m / 2^10 + experts*m / 2^4 tiles, below 2^30 + 2^36 / 144 (a row has 144
+    // bytes or more), and an item's last, partial tile of rows.  The one-tile form
+    // runs for a mean below 16 slots only, with fewer than 2*experts items; the
+    // binary16 kernels' tiles are 128 rows of 64 slots.
     rc = check_device();
     if (rc != MMQ_OK) return rc;
     const uint8_t* wb = static_cast<const uint8_t*>(w);

@@ -128,3 +128,26 @@ def test_combine_past_2_31_values():
     for a in range(0, n, 1 << 16):   # one expert: a single product, rounded once
         part = slice(a, a + (1 << 16))
         assert torch.equal(out[part], weight[part] * y[slot[part, 0].long()].float()), a
+
+
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+def test_grouped_output_of_2_35_values(fmt):
+    """Where one slot per item and 16 rows per tile would be more than 2^31
+    tiles (the kernels' items are larger)."""
+    m, k, slots, pool = 16384, 256, 1 << 21, 64
+    note("large grouped output, 2^35 values, %s" % fmt)
+    w = [refs.weights(fmt, 62 + i, m, k) for i in range(2)]
+    dw = to_dev(np.concatenate([x.reshape(-1) for x in w]))
+    q, ds = oracle.quantize(synth.random_activations(4, pool, k, "outliers"))
+    dq, dds = to_dev(q), to_dev(ds.view(np.int32))
+    rows = torch.randint(0, pool, (slots,), dtype=torch.int32, device=DEV)
+    cut = slots - 300
+    f = binding.FORMAT_Q4K if fmt == "q4k" else binding.FORMAT_Q6K
+    out = binding.fold_grouped(f, dw, 2, m, k, dq, dds, to_dev(np.array([0, cut, slots], np.int32)), rows, f16=True)
+    idx = torch.arange(pool, dtype=torch.int32, device=DEV).repeat(5)
+    for e, (a, b) in enumerate(((0, cut), (cut, slots))):
+        off = [0, pool * 5, pool * 5] if e == 0 else [0, 0, pool * 5]
+        small = binding.fold_grouped(f, dw, 2, m, k, dq, dds, to_dev(np.array(off, np.int32)), idx)[:pool].clone()
+        torch.cuda.synchronize()
+        check_fp32(small.cpu().numpy(), refs.fold64(fmt, w[e], m, k, q, ds), "pool")
+        _same_rows(out[a:b], small.half(), rows[a:b].long(), "expert %d" % e)
