@@ -466,7 +466,10 @@ int moe_route(const float *logits, int64_t n, int64_t experts, int64_t stride, i
  *   slot, weights : [n][top] from moe_route, top <= 64.
  *   residual : float [n][m] or NULL; may be out itself.
  *   out      : float [n][m] (out).
- * n or m of 0 is an empty call.
+ * n or m of 0 is an empty call.  Limits: slots*m and n*m below 2^40, n*top at
+ * most 2^30, and n*c below 2^24 for c workgroups on a token's columns, c =
+ * ceil(m/2048) for binary16 y and m a multiple of 8, ceil(m/1024) for float y and
+ * m a multiple of 4, else ceil(m/256).
  */
 int moe_combine(const void *y, int y_f16, int64_t slots, int64_t m, const int32_t *slot, const float *weights,
                 int64_t n, int top, const float *residual, float *out, hipStream_t stream);

@@ -56,6 +56,12 @@ constexpr int kRouteMaxExperts = 1024, kRouteMaxTop = 64;
 hipError_t launch_route(const float* logits, int64_t stride, int n, int experts, int top, bool normalize, float scale,
                         int32_t* ids, float* weights, int32_t* slot, int32_t* rows, int32_t* offsets,
                         hipStream_t stream);
+// Workgroups of 256 threads on a token's m columns: 16 bytes of y per thread
+// where m is a multiple of that many values, else one value.
+inline int64_t combine_cols(bool y_f16, int64_t m) {
+    const int64_t vec = y_f16 ? 8 : 4, per = 256 * (m % vec == 0 ? vec : 1);
+    return (m + per - 1) / per;
+}
 hipError_t launch_combine(const void* y, bool y_f16, int64_t slots, int m, const int32_t* slot, const float* weights,
                           int n, int top, const float* residual, float* out, hipStream_t stream);
 

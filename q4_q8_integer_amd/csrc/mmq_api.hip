@@ -684,7 +684,7 @@ int moe_combine(const void* y, int y_f16, int64_t slots, int64_t m, const int32_
     if (slots < 0 || n < 0 || m < 0 || top <= 0) return MMQ_ERR_SHAPE;
     if (slots > kMaxDim || n > kMaxDim || m > kMaxDim || top > mmq::kRouteMaxTop) return MMQ_ERR_OVERFLOW;
     if (slots * m >= kMaxElems || n * m >= kMaxElems || n * top > kMaxRouteIds) return MMQ_ERR_OVERFLOW;
-    if (!threads_ok(n * ((m + 255) / 256), 256)) return MMQ_ERR_OVERFLOW;
+    if (!threads_ok(n * mmq::combine_cols(y_f16 != 0, m), 256)) return MMQ_ERR_OVERFLOW;
     if (n == 0 || m == 0) return MMQ_OK;
     if ((slots > 0 && !y) || !slot || !weights || !out) return MMQ_ERR_NULL;
     if (!opt_aligned16(y) || !aligned16(slot) || !aligned16(weights) || !opt_aligned16(residual) || !aligned16(out))

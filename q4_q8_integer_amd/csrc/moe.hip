@@ -358,7 +358,7 @@ template <bool H>
 hipError_t launch_combine_t(const void* y, int64_t slots, int m, const int32_t* slot, const float* weights, int n,
                             int top, const float* residual, float* out, hipStream_t stream) {
     const bool vec = m % YVec<H>::kN == 0;
-    const int per = 256 * (vec ? YVec<H>::kN : 1), cols = (m + per - 1) / per;
+    const int cols = (int)combine_cols(H, m);
     const dim3 grid((unsigned)((int64_t)n * cols));
     if (vec)
         hipLaunchKernelGGL((combine_kernel<H, true>), grid, dim3(256), 0, stream, y, slots, m, slot, weights, top, cols,

@@ -37,3 +37,22 @@ def test_grouped_limits(lib, fmt):
     assert grouped(lib, fmt, 4096, 8 << 18, 256, 64, 64) == OVERFLOW           # 2^33: past 2^40 bytes
     assert grouped(lib, fmt, 2, 64, 256, (1 << 24) - 1, 64) == DEVICE          # tokens*k just below 2^32
     assert grouped(lib, fmt, 2, 64, 256, 1 << 24, 64) == OVERFLOW
+
+
+def combine(lib, f16, slots, m, n, top=2):
+    return lib.moe_combine(A, f16, slots, m, A, A, n, top, 0, A, None)
+
+
+def test_combine_limits(lib):
+    assert combine(lib, 1, 64, 4096, 1 << 20) == DEVICE          # 2 workgroups a token
+    assert combine(lib, 1, 64, 4096, (1 << 23) - 1) == DEVICE
+    assert combine(lib, 1, 64, 4096, 1 << 23) == OVERFLOW        # 2^24 workgroups
+    assert combine(lib, 0, 64, 4096, (1 << 22) - 1) == DEVICE
+    assert combine(lib, 0, 64, 4096, 1 << 22) == OVERFLOW
+    assert combine(lib, 1, 64, 100, (1 << 24) - 1) == DEVICE     # 4 values over: a value per thread
+    assert combine(lib, 1, 64, 4097, 1 << 20) == OVERFLOW        # 17 workgroups a token
+    assert combine(lib, 0, 64, 64, (1 << 24) - 1, top=64) == DEVICE
+    assert combine(lib, 0, 64, 64, 1 << 24, top=64) == OVERFLOW
+    for m in ((1 << 31) - 1, (1 << 31) - 4, (1 << 31) - 8):      # columns up to the last int
+        assert combine(lib, 0, 1, m, 1, 1) == DEVICE
+        assert combine(lib, 1, 1, m, 1, 1) == DEVICE

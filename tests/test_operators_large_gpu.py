@@ -151,3 +151,32 @@ def test_grouped_output_of_2_35_values(fmt):
         torch.cuda.synchronize()
         check_fp32(small.cpu().numpy(), refs.fold64(fmt, w[e], m, k, q, ds), "pool")
         _same_rows(out[a:b], small.half(), rows[a:b].long(), "expert %d" % e)
+
+
+@pytest.mark.parametrize("f16,m", [(True, 2 ** 31 - 1), (True, 2 ** 31 - 8), (False, 2 ** 31 - 4)])
+def test_combine_columns_up_to_the_last_int(f16, m):
+    """Rows of nearly 2^31 columns, where m and a workgroup's columns together
+    pass an int: by value and by 16 bytes."""
+    note("combine m=%d" % m)
+    y = (torch.arange(m, device=DEV, dtype=torch.int32) % 2039).to(torch.float16 if f16 else torch.float32)[None, :]
+    out = torch.full((1, m), 7.0, device=DEV)
+    got = binding.combine(y, torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.full((1, 1), 0.5, device=DEV),
+                          out=out)
+    torch.cuda.synchronize()
+    assert got is out
+    for a in range(0, m, 1 << 28):
+        part = slice(a, min(a + (1 << 28), m))
+        assert torch.equal(out[0, part], 0.5 * y[0, part].float()), a
+
+
+def test_combine_of_2_32_values():
+    m, n, slots = 4096, (1 << 20) + 3, 70
+    note("combine n=%d m=%d" % (n, m))
+    y = torch.randn(slots, m, device=DEV).half()
+    slot = torch.randint(0, slots, (n, 1), dtype=torch.int32, device=DEV)
+    weight = torch.rand(n, 1, device=DEV)
+    out = binding.combine(y, slot, weight)
+    torch.cuda.synchronize()
+    for a in range(0, n, 1 << 16):   # one expert: a single product, rounded once
+        part = slice(a, a + (1 << 16))
+        assert torch.equal(out[part], weight[part] * y[slot[part, 0].long()].float()), a
