@@ -448,8 +448,8 @@ int mmq_fold_grouped(int format, const void *w, int64_t experts, int64_t m, int6
  *   offsets : int32 [experts + 1] (out), as mmq_fold_grouped takes them.
  * Deterministic, no workspace.  n == 0 is an empty call (offsets too stay as
  * they are).  MMQ_ERR_SHAPE for top outside 1 .. experts or a stride below
- * experts; MMQ_ERR_OVERFLOW for experts above 1024, top above 64, or n*top
- * above 2^30.
+ * experts; MMQ_ERR_OVERFLOW for experts above 1024, top above 64, n above
+ * 2^26 - 4 (a wave per token), or n*top above 2^30.
  */
 int moe_route(const float *logits, int64_t n, int64_t experts, int64_t stride, int top, int normalize, float scale,
               int32_t *ids, float *weights, int32_t *slot, int32_t *rows, int32_t *offsets, hipStream_t stream);

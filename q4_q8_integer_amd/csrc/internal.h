@@ -53,6 +53,7 @@ hipError_t launch_norm(const NormArgs& a, int n, int k, int8_t* q, uint16_t* qt,
 
 // Router and combination of the matmuls grouped by expert (moe.hip).
 constexpr int kRouteMaxExperts = 1024, kRouteMaxTop = 64;
+constexpr int kTopkWaves = 4;   // tokens per workgroup of the choosing kernel, a wave each
 hipError_t launch_route(const float* logits, int64_t stride, int n, int experts, int top, bool normalize, float scale,
                         int32_t* ids, float* weights, int32_t* slot, int32_t* rows, int32_t* offsets,
                         hipStream_t stream);

@@ -667,7 +667,8 @@ int moe_route(const float* logits, int64_t n, int64_t experts, int64_t stride, i
     int64_t s = 0;
     const int rc = row_stride(stride, experts, n, &s);
     if (rc != MMQ_OK) return rc;
-    if (n > kMaxDim || n * top > kMaxRouteIds || !threads_ok(n, 64)) return MMQ_ERR_OVERFLOW;   // a wave per token
+    if (n > kMaxDim || n * top > kMaxRouteIds) return MMQ_ERR_OVERFLOW;
+    if (!threads_ok((n + mmq::kTopkWaves - 1) / mmq::kTopkWaves, 64 * mmq::kTopkWaves)) return MMQ_ERR_OVERFLOW;
     if (n == 0) return MMQ_OK;
     if (!logits || !ids || !weights || !slot || !rows || !offsets) return MMQ_ERR_NULL;
     if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(slot) || !aligned16(rows) ||

@@ -34,8 +34,6 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr int kTopkWaves = 4;
-
 // One step of a wave reduction: v of the lane that CTRL names, or `other` in
 // lanes that have none.
 template <int CTRL>

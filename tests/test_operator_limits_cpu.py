@@ -56,3 +56,14 @@ def test_combine_limits(lib):
     for m in ((1 << 31) - 1, (1 << 31) - 4, (1 << 31) - 8):      # columns up to the last int
         assert combine(lib, 0, 1, m, 1, 1) == DEVICE
         assert combine(lib, 1, 1, m, 1, 1) == DEVICE
+
+
+def test_route_limits(lib):
+    def route(n, experts, top):
+        return lib.moe_route(A, n, experts, 0, top, 1, 1.0, A, A, A, A, A, None)
+    assert route((1 << 26) - 4, 2, 1) == DEVICE
+    for more in (3, 2, 1, 0):                       # 2^24 workgroups of 4 waves
+        assert route((1 << 26) - more, 2, 1) == OVERFLOW
+    assert route(1 << 24, 64, 64) == DEVICE         # 2^30 choices
+    assert route((1 << 24) + 1, 64, 64) == OVERFLOW
+    assert route(5, 1024, 64) == DEVICE

@@ -180,3 +180,24 @@ def test_combine_of_2_32_values():
     for a in range(0, n, 1 << 16):   # one expert: a single product, rounded once
         part = slice(a, a + (1 << 16))
         assert torch.equal(out[part], weight[part] * y[slot[part, 0].long()].float()), a
+
+
+def test_route_of_the_most_tokens():
+    """2^26 - 4 tokens, the launch's limit, two experts."""
+    n = (1 << 26) - 4
+    note("route n=%d" % n)
+    logits = torch.randn(n, 2, device=DEV)
+    logits[::9] = -float("inf")
+    r = binding.route(logits, 1)
+    live, second = logits[:, 0] > -float("inf"), logits[:, 1] > logits[:, 0]
+    torch.cuda.synchronize()
+    ids = torch.where(live, second.int(), -1)
+    assert torch.equal(r.ids[:, 0], ids)
+    assert torch.equal(r.weights[:, 0], live.float())
+    first, used = int((ids == 0).sum()), int(live.sum())
+    assert r.offsets.tolist() == [0, first, used]
+    rows = torch.cat([(ids == e).nonzero()[:, 0] for e in (0, 1)]).int()
+    assert torch.equal(r.rows[:used], rows) and (r.rows[used:] == -1).all()
+    slot = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    slot[rows.long()] = torch.arange(used, dtype=torch.int32, device=DEV)
+    assert torch.equal(r.slot[:, 0], slot)
