@@ -627,7 +627,8 @@ def quantize_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, y=No
     """q8 of the normed residual stream (q8_quantize_norm): (q int8 [n, k],
     ds int32 [n, k/32], r).  x float32 [n, k]; y float32 or binary16 [n, k];
     gate [k] or [n, k]; r: where the new stream goes (x itself is fine), x
-    without y; h: a float32 [n, k] that gets the normed values too."""
+    without y; h: a float32 [n, k] that gets the normed values too.  A token
+    with a NaN or an infinity gets NaN scales, and its products are NaN."""
     a, n, k, r = _norm_args(x, weight, eps, y, y_weight, gate, residual_scale, r, h)
     q = torch.empty((n, k), dtype=torch.int8, device=x.device)
     ds = torch.empty((n, k // 32), dtype=torch.int32, device=x.device)

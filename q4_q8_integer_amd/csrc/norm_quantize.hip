@@ -42,6 +42,8 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 enum { kNoY = 0, kY32 = 1, kY16 = 2 };
 enum { kNoCodes = 0, kRows = 1, kTiles = 2 };
 
+constexpr uint32_t kNanScale = 0x7E00u;   // a scale word: binary16 NaN, sum of codes 0
+
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     const v4f a = *reinterpret_cast<const v4f*>(p), b = *reinterpret_cast<const v4f*>(p + 4);
 #pragma unroll
@@ -117,7 +119,14 @@ __device__ __forceinline__ void emit(const NormArgs& a, int row, int col, int k,
     if (a.h) store8(a.h + (int64_t)row * k + col, h);
     if (OUT == kNoCodes) return;
     uint32_t packed[2];
-    const uint32_t word = q8_block(h, packed);
+    uint32_t word = q8_block(h, packed);
+    // The quantizer's maximum passes over a NaN.  Here one NaN or infinity in a
+    // token makes all its h NaN or 0, which would be a scale of 0 and a product
+    // of 0, so a block with a NaN gets a NaN scale.
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) nan |= __builtin_isunordered(h[i], h[i + 1]);
+    if ((__ballot(nan) >> (threadIdx.x & 60)) & 15) word = kNanScale;   // of the quad's 32 values
     const int c = col >> 5, part = (col >> 3) & 3, C = k >> 5;
     if (OUT == kTiles)
         *reinterpret_cast<uint4*>(qt + q8_slot(row, c, part, C) * 8) = q8_slot_value(packed);
