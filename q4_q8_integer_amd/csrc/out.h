@@ -12,10 +12,11 @@
 // run-time values: per output they cost a few scalar branches in kernels
 // that spend k / 32 vector operations on it, where a template per choice
 // would multiply every kernel by 40.  Measured: 4096 x 4096, 2630 tokens, fold
-// 161-170 us, with bias and float32 residual 172 (the residual's 43 MB are 8 us
-// at the copy rate), with bias and SiLU 170 (184 with an exponential and a
-// division of full range), GELU 180 (the consumer waves' last step); 28672 x
-// 8192, 7 tokens, 30-31 us with any of them, as the fold.
+// 161-177 us, with bias and float32 residual 180 (the residual's 43 MB are 8 us
+// at the copy rate), with bias and SiLU 177 (173 with the hardware's
+// exponential alone, 184 with a full division too), GELU 182 (the consumer
+// waves' last step); 28672 x 8192, 7 tokens, 29-31 us with any of them, as the
+// fold.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -49,14 +50,13 @@ struct OutF16 {
 
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-// v * sigmoid(x) = v / (1 + exp(-x)) on the hardware's exponential and
-// reciprocal (one ulp each), five instructions.  The product with log2(e) is
-// rounded once, which moves the result as a rounding of x does: by |x| 2^-24
-// of it in the lower tail, less above.  Below x = -88 the exponential
-// overflows and the result is -0, as the exact value (below 1e-36) is to 36
-// digits.
+// v * sigmoid(x) = v / (1 + exp(-x)), the exponential and the hardware's
+// reciprocal to an ulp each.  (The hardware's exponential on x * log2(e)
+// rounded once is 4 instructions less but off by up to |x| steps in the lower
+// tail.)  Below x = -87 the reciprocal leaves float32's normal range and the
+// result may be -0 for an exact value below 1.1e-36.
 __device__ __forceinline__ float times_sigmoid(float v, float x) {
-    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
+    return v * __builtin_amdgcn_rcpf(1.0f + expf(-x));
 }
 
 __device__ __forceinline__ float activate(float v, int act) {
