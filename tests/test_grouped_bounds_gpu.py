@@ -70,3 +70,63 @@ def test_decreasing_offsets_of_many_experts(n):
     out = out.cpu().numpy()
     check_fp32(out[:n - 1], p.fold(63, rows[:n - 1]), "expert 63")
     check_fp32(out[n - 1:], p.fold(130, rows[n - 1:]), "the last expert")
+
+
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+@pytest.mark.parametrize("n", [9, 30, 200])
+def test_rows_out_of_range_on_both_sides(fmt, n):
+    """Rows below 0 count as the first row of q, rows past its end as the last,
+    in every kernel's range."""
+    p = Problem(fmt, 2, 40, 512, 12, 3)
+    rows = np.random.default_rng(n).integers(0, 12, n + 5)
+    bad = np.array([-5, 1 << 30, 12, -1, -(1 << 31), (1 << 31) - 1])
+    rows[2:n:2] = bad[np.arange(len(rows[2:n:2])) % 6]
+    note("grouped rows out of range %s n=%d" % (fmt, n))
+    out = p.call([0, n, n + 5], rows)
+    torch.cuda.synchronize()
+    at = np.clip(rows, 0, 11)
+    check_fp32(out[:n].cpu().numpy(), p.fold(0, at[:n]), "clamped")
+    check_fp32(out[n:].cpu().numpy(), p.fold(1, at[n:]), "in range")
+
+
+# The kernels' borders: 16 slots (one token tile), 32 (q4_K) and 64 (q6_K), 64
+# and 128 (binary16 items), with the mean below 16 slots, where the one-tile
+# form is launched, and above.
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+@pytest.mark.parametrize("counts", [[15, 0, 31], [16, 32, 0, 0, 0, 0], [17, 33, 0, 0, 0, 0], [31, 32, 33], [16, 17, 15, 32],
+                                    [32], [33], [63, 64, 65], [64, 0, 0, 0, 0, 0], [65, 0, 0, 0, 0, 0], [127, 128, 129],
+                                    [95, 97], [32, 33, 64, 65, 1, 16, 17, 2, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0]], ids=str)
+def test_groups_at_the_kernels_borders(fmt, counts):
+    p = Problem(fmt, len(counts), 72, 768, 50, 4)
+    rows = np.random.default_rng(sum(counts)).integers(0, 50, sum(counts))
+    off = np.concatenate(([0], np.cumsum(counts)))
+    note("grouped borders %s %s" % (fmt, counts))
+    out = p.call(off, rows)
+    torch.cuda.synchronize()
+    out = out.cpu().numpy()
+    for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        if a < b:
+            check_fp32(out[a:b], p.fold(e, rows[a:b]), "expert %d" % e)
+
+
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+def test_rows_of_codes_past_2_31_bytes(fmt):
+    """Gathered rows on both sides of 2^31 bytes of codes and up to the 2^32
+    that are allowed, where byte offsets pass an int; in each kernel."""
+    m, k, pool = 24, 4096, 64
+    tokens = (1 << 20) - 1
+    assert 1 << 31 < tokens * k < 1 << 32
+    note("grouped codes past 2^31 bytes %s" % fmt)
+    p = Problem(fmt, 3, m, k, pool, 5)
+    p.dq = p.dq.repeat((tokens + pool - 1) // pool, 1)[:tokens].contiguous()
+    p.dds = p.dds.repeat((tokens + pool - 1) // pool, 1)[:tokens].contiguous()
+    counts = [12, 30, 200]
+    rng = np.random.default_rng(7)
+    rows = rng.integers(tokens // 2 - 3, tokens, sum(counts))
+    rows[[0, 12, 42]], rows[[1, 13, 43]] = tokens - 1, (1 << 19) - 1
+    off = np.concatenate(([0], np.cumsum(counts)))
+    out = p.call(off, rows)
+    torch.cuda.synchronize()
+    for e in range(3):
+        a, b = off[e], off[e + 1]
+        check_fp32(out[a:b].cpu().numpy(), p.fold(e, rows[a:b] % pool), "expert %d" % e)
