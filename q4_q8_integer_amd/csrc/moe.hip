@@ -12,12 +12,17 @@
 //     and, per wave over a contiguous run, those equal to e, then goes over
 //     the run again, 256 ids at a time, and writes slots and rows where there
 //     are any.  Slots of an expert are in token order.
-//   * With at most kSmallIds ids (a decode step) one workgroup does both in
-//     one launch, the ids in LDS: each id's slot is the number of ids below
-//     it and of equal ones before it, counted by four lanes.
-// Measured: 16 tokens, 8 of 64 experts 6.5 us in a graph and 14 us a call
-// from Python (two launches 6.1 and 17); 8192 tokens, 8 of 128 experts 22 us
-// (8 us choosing, 14 sorting), where the 5 MB moved take 1 us.
+//   * A decode step's few ids (at most kSmallIds, times the rounds in which the
+//     16 waves take the tokens) are chosen and sorted by one workgroup in one
+//     launch, the ids in LDS: each id's slot is the number of ids below it and
+//     of equal ones before it, counted by four lanes.
+// Measured in a graph, one launch against two, 64 / 1024 experts: 1 token of 8
+// experts 3.6 / 8.0 us against 5.8 / 12.2, 16 of 4 4.8 / 9.0 against 5.6 / 10.7,
+// 16 of 8 (128 ids) 6.8 / 14.0 against 6.2 / 12.8, where a call from Python is
+// 13.6 against 16.5 us; 32 of 2 5.4 / 10.4 against 5.5 / 9.4; beyond the rule 16
+// of 16 11 / 26 against 7.1 / 17, 32 of 8 12 / 27 against 6.1 / 12.8.
+// 8192 tokens, 8 of 128 experts 22 us: 8 us choosing, 14 sorting, where the 5 MB
+// moved take 1 us: every expert's workgroup reads all ids, once or twice.
 //
 // Combining: out[t] = residual[t] + sum_j weights[t][j] * y[slot[t][j]], a
 // thread per 16 bytes of y columns; slots and weights of a token are the
@@ -134,7 +139,7 @@ __global__ __launch_bounds__(64 * kTopkWaves) void route_topk_kernel(const float
 }
 
 // The whole routing of up to kSmallIds ids, in one workgroup.
-constexpr int kSmallIds = 256, kSmallThreads = 1024;
+constexpr int kSmallIds = 128, kSmallThreads = 1024;
 template <int J>
 __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(const float* __restrict__ logits, int64_t stride,
                                                                     int n, int experts, int top, int normalize,
@@ -372,7 +377,8 @@ hipError_t launch_route_t(const float* logits, int64_t stride, int n, int expert
                           int32_t* ids, float* weights, int32_t* slot, int32_t* rows, int32_t* offsets,
                           hipStream_t stream) {
     const int count = n * top;
-    if (count <= kSmallIds) {
+    const int rounds = (n + kSmallThreads / 64 - 1) / (kSmallThreads / 64);   // of the small kernel's waves
+    if ((int64_t)count * rounds <= kSmallIds) {
         hipLaunchKernelGGL((route_small_kernel<J>), dim3(1), dim3(kSmallThreads), 0, stream, logits, stride, n, experts,
                            top, (int)normalize, scale, ids, weights, slot, rows, offsets);
         return hipGetLastError();
