@@ -343,8 +343,10 @@ enum mmq_format {
 /*
  * mmq_kernel_choice - the kernel (enum mmq_kernel, never MMQ_KERNEL_AUTO)
  * that the fold entry point of `format` runs for an m x k weight and n
- * tokens; host logic only, no HIP call.  MMQ_ERR_SHAPE for negative sizes or
- * k not a positive multiple of 256, MMQ_ERR_KERNEL for an unknown format.
+ * tokens; host logic only, no HIP call.  (mmq_fold_epilogue runs the same but
+ * for MMQ_FORMAT_Q6K, see there; its kernels and those of mmq_fold_grouped have
+ * no id.)  MMQ_ERR_SHAPE for negative sizes or k not a positive multiple of 256,
+ * MMQ_ERR_KERNEL for an unknown format.
  */
 int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n);
 
@@ -358,10 +360,10 @@ int mmq_kernel_choice(int format, int64_t m, int64_t k, int64_t n);
  * where fold is the float32 result of the entry point of `format` for the
  * same arguments, bit for bit (with every operand absent and MMQ_ACT_NONE the
  * call is that entry point), except MMQ_FORMAT_Q6K at 9 to 64 tokens, and above
- * while ceil(m/16)*ceil(n/64) <= 1536 (and n*k < 2^32), which runs kernels of its own with the
- * same accuracy.  Outputs and residuals may be
- * rows of larger arrays (strides), and the residual may be the output itself
- * (same type and stride: x += W h); otherwise they must not overlap.
+ * while ceil(m/16)*ceil(n/64) <= 1536 (and n*k < 2^32), which runs kernels of
+ * its own with the same accuracy.  Outputs and residuals may be rows of larger
+ * arrays (strides), and the residual may be the output itself (same type and
+ * stride: x += W h); otherwise they must not overlap.
  *
  *   w, q, ds : as for the entry point of `format` (q: its int8 codes or its
  *              operand tiles); m, k, n and their limits too.

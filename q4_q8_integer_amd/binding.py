@@ -712,8 +712,9 @@ def fold_grouped(fmt: int, w: torch.Tensor, experts: int, m: int, k: int, q: tor
     binary16 [slots, m].  w: experts matrices of m x k (FORMAT_Q4K or
     FORMAT_Q6K); offsets int32 [experts + 1]; rows int32 [slots], the row of q
     of each slot, or None (slot s takes row s); bias [experts, m].  slots is
-    out's rows, else those of rows, else those of q; rows of out that belong
-    to no expert are left as they were (uninitialised in a new tensor)."""
+    the length of rows, or the rows of q without it, and no more than out has;
+    rows of out that belong to no expert are left as they were (uninitialised
+    in a new tensor).  residual [slots, m] may be out."""
     if fmt not in (FORMAT_Q4K, FORMAT_Q6K):
         raise ValueError("grouped products take FORMAT_Q4K or FORMAT_Q6K, got %r" % (fmt,))
     if experts < 1:

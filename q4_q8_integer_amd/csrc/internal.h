@@ -180,8 +180,9 @@ hipError_t launch_f16_grouped(const uint8_t* w, int m, int k, const int8_t* q, c
                               const OutEpi& out, int tokens_per_item, hipStream_t stream);
 // Slots of an expert up to which the streaming kernel (mmq_group_few.hip) takes
 // it, in its form with one tile of 16 tokens and in the other one.  Against the
-// binary16 kernel, 64 experts of 1536 x 4096 in q4_K: 32 slots 111 us (140),
-// 33 slots 136 (124); of 4096 x 1536 in q6_K: 64 slots 268 us (316).
+// binary16 kernel, 64 experts of 1536 x 4096 in q4_K: 32 slots 105 us (117),
+// 33 slots 129 (116); of 4096 x 1536 in q6_K: 64 slots 261 us (312), 65 slots
+// 490 (315).
 constexpr int kGroupFewMaxTile = 16, kGroupFewMaxQ4k = 32, kGroupFewMaxQ6k = 64;
 hipError_t launch_few_grouped(bool q6k, const uint8_t* w, int m, int k, const int8_t* q, const uint32_t* ds,
                               const Groups& g, const OutEpi& out, hipStream_t stream);

@@ -35,14 +35,16 @@
 //     decoded once for all their tiles; its copy addresses are computed anew,
 //     which leaves the loop its registers.
 //
-// Measured (graph of calls): q4_K, 14336 x 4096, 2 / 8 experts of 2 slots 20 /
-// 64-70 us (weights alone at the copy rate 13 / 52), 8 of 16 83, of 32 120; 64
-// experts of 1536 x 4096 at 2 / 16 / 32 slots 56 / 73 / 105 us (44 / 46 / 48);
-// q6_K, 64 of 4096 x 1536 at 1 / 16 / 32 / 64 slots 90 / 104 / 162 / 270 us (64 /
-// 68 / 71 / 79).  Up to 16 slots the weights stream at 3 to 4.2 TB/s (with the
+// Measured (graph of calls): q4_K, 14336 x 4096, 2 / 8 experts of 2 slots 18 /
+// 66-72 us (weights alone at the copy rate 13 / 52), 8 of 16 82, of 32 121; 64
+// experts of 1536 x 4096 at 4 / 16 / 32 slots 58 / 73 / 105 us (45 / 46 / 48);
+// q6_K, 64 of 4096 x 1536 at 1 / 16 / 32 / 64 slots 85-90 / 104 / 157 / 261 us (64
+// / 68 / 71 / 79).  Up to 16 slots the weights stream at 3 to 4.3 TB/s (with the
 // codes of 4 tokens only and two steps in flight no faster, so not for want of
 // copies in flight); above, vector issue bounds it (per 16 x 16 outputs and
-// chunk 8 operations in q4_K, 16 in q6_K, and the decode).
+// chunk 8 operations in q4_K, 16 in q6_K, and the decode): at 32 slots in q4_K
+// the vector unit is busy 72% of the time and the matrix core 15%, at 64 in q6_K
+// 80% and 16%.
 #include <algorithm>
 #include <type_traits>
 

@@ -12,8 +12,8 @@
 //     tokens (A) x 16 rows (B).  The two groups' dots come from two MFMAs on
 //     the same tokens, the weights of the lanes of the other group set to 0
 //     (lane l holds row l % 16 and k = 8 (l / 16) .. +7: lanes 0-31 are the
-//     first group).  Half the matrix work is zeros; the vector unit, not the
-//     matrix core, is what bounds this kernel.
+//     first group).  Half the matrix work is zeros; the matrix core is the
+//     least busy unit all the same.
 //   * The output column of a lane is its own weight row, so the scales are
 //     per-lane integers: I = sc0*D0 + sc1*D1 is exact (two 24-bit
 //     multiply-adds, |I| <= 2^24), then acc_b += da * float(I): 4 vector
@@ -28,10 +28,12 @@
 //     bookkeeping; one wait for everything opens each step.
 //   * The 8 partial sums are added in LDS in a fixed order.
 //
-// Bound by vector issue: per chunk and 16 x 16 outputs 16 operations (and 24
-// per chunk for the decode, shared by the token tiles).  4096 x 11008 at 16 /
-// 33 / 64 tokens 14.6 / 26.6 / 32.5 us (weights at the copy rate 7.2; the
-// binary16 kernel 225).
+// 4096 x 11008 at 16 / 33 / 64 tokens 14.9 / 27 / 33 us (weights at the copy rate
+// 7.2; the binary16 kernel 203).  Nothing is full: at 33 / 64 tokens the vector
+// unit is busy 49 / 54% of the time (16 operations per chunk and 16 x 16 outputs,
+// and 24 per chunk for the decode, shared by the token tiles), the matrix core
+// 11 / 13%, and HBM gives 1.5 TB/s; the two waves of a SIMD do not cover each
+// other's waits.
 #include "f16_operand.h"
 #include "internal.h"
 #include "kquant_device.h"

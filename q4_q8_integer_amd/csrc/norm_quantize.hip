@@ -22,9 +22,10 @@
 // (or x) again, from cache, for the second norm.
 //
 // Measured: 8192 rows of 4096, y in binary16 with its norm, a gate per channel
-// and h out, 99 us (470 MB: 91 us at the copy rate; HBM bound).  One row of 4096
-// with codes 4 us in a graph, a launch and two reductions across 8 waves; 22 us
-// a call from Python, three allocations among them.
+// and h out, 99 us (470 MB: 91 us at the copy rate; HBM bound); y in float32, no
+// operands, with codes as rows 83 us (440 MB: 86), as operand tiles 108 (474 MB:
+// 92).  One row of 4096 with codes 4 us in a graph, a launch and two reductions
+// across 8 waves; 22 us a call from Python, three allocations among them.
 //
 // With operand tiles a lane's codes are one 16-byte slot, and the slots of
 // consecutive tokens are adjacent: eight consecutive rows go to the same XCD

@@ -130,3 +130,31 @@ def test_rows_of_codes_past_2_31_bytes(fmt):
     for e in range(3):
         a, b = off[e], off[e + 1]
         check_fp32(out[a:b].cpu().numpy(), p.fold(e, rows[a:b] % pool), "expert %d" % e)
+
+
+@pytest.mark.parametrize("fmt", ["q4k", "q6k"])
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("m,pad", [(72, 0), (72, 8), (40, 3)])
+def test_residual_in_place(fmt, f16, m, pad):
+    """x += the experts' products, in the output's own rows (of a wider array
+    too), in every kernel: each value is read and written once, and rows
+    outside the groups and columns beside them keep theirs."""
+    counts = [9, 30, 0, 70, 150]
+    p = Problem(fmt, len(counts), m, 512, 30, 6)
+    n = sum(counts) + 7
+    rng = np.random.default_rng([m, pad, f16])
+    rows = rng.integers(0, 30, n)
+    off = 4 + np.concatenate(([0], np.cumsum(counts)))
+    dt = torch.float16 if f16 else torch.float32
+    note("grouped in place %s f16=%s m=%d pad=%d" % (fmt, f16, m, pad))
+    used = slice(off[0], off[-1])
+    plain = p.call(off, rows)[used].cpu().numpy()
+    x = rng.standard_normal((n, m + pad)).astype(np.float16 if f16 else np.float32)
+    buf = to_dev(x)
+    out = buf[:, :m]
+    assert p.call(off, rows, residual=out, out=out, f16=f16) is out
+    torch.cuda.synchronize()
+    got = buf.cpu().numpy()
+    assert np.array_equal(got[:, m:], x[:, m:])
+    assert np.array_equal(got[:off[0]], x[:off[0]]) and np.array_equal(got[off[-1]:], x[off[-1]:])
+    refs.check_epilogue(got[used, :m], plain, None, 0, x[used, :m], f16, "in place")
