@@ -490,8 +490,9 @@ int moe_combine(const void *y, int y_f16, int64_t slots, int64_t m, const int32_
  * evaluated in float64 between the roundings named, means over the k values
  * of a token.  A NaN or an infinity in a token's x or y makes its h NaN or 0
  * throughout; a 32-value block whose h has a NaN gets a NaN da (and any codes),
- * so that every product of the token is NaN, not 0.  Without y the stream is not changed: r = x, and y_weight, gate
- * and r must be NULL and residual_scale 1 (MMQ_ERR_NULL).
+ * so that every product of the token is NaN, not 0.  Without y the stream is
+ * not changed: r = x, and y_weight, gate and r must be NULL and residual_scale
+ * 1 (MMQ_ERR_NULL).
  *
  *   n, k     : k % 32 == 0; limits as for q8_quantize_rows, n at most 2^31 - 128
  *              and n*1024 below 2^32.
