@@ -15,7 +15,9 @@
 //   O^T = V^T P  16 dims x 16 rows, 32 keys an instruction: codes as binary16
 //                (exact), the weights p * (scale of the value's block) as
 //                binary16 where q and out are (a rounding of 2^-11, as the
-//                output's own), else as hi + lo (22 bits)
+//                output's own: 2.9e-4 from 64 bits where the output's alone is
+//                2.1e-4), else as hi + lo (22 bits).  hi + lo there too takes 723
+//                us for 505 (prompt chunk), 141 for 124 (own heads, 4 bits)
 //
 // so all sums are float32.  S^T leaves a lane with 4 keys of each half of its
 // 32, of one row; the second product takes its k index in that order, so
@@ -23,12 +25,17 @@
 // 4 + 4 keys, two words a block pair, that mixed-precision multiply-adds take
 // as they are.
 //
-// The softmax keeps a running reference m per row; sums and weights are of
-// exp2(s - m - e), and m moves (everything so far is rescaled) only when a
-// score exceeds it by 2^10, which few steps do: those leave the inner loop.  e
-// does the same for the values' scales: 2^e bounds those that the row has seen
-// within a factor of 4, and with it weights stay below 2^15.  Weights of 2^-14
-// and less lose bits, absolute 2^-25: a token 2^14 times below e's level.
+// The softmax keeps a running reference r per row; sums and weights are of
+// exp2(s - r).  What binary16 has to hold is a weight times its value's scale, so
+// r goes by the largest such product of a step: it is put 2^5 below that, and moves
+// (everything so far is rescaled) only when a product may pass binary16's range,
+// or when the step's largest score is 2^8 below that of the step that set it.
+// Few steps do either: those leave the inner loop.  Products lose bits below
+// 2^-14, by 2^-25 absolutely: 2^-21 of the step's largest weight times the
+// largest value that the row has seen, whatever far larger weight (of a first token
+// whose values are small, say) came before.  1200 tokens that share 2^-17 of the weight
+// beside one without a value: 3e-7 off in float32, 4% with a reference that only rises
+// with the scores (level in time but for some steps more: prompt chunk 513 and 516 us).
 //
 // Few rows (kNarrow, kWide) are bound by the cache: every wave has its own steps,
 // copied straight into LDS while the step before is worked on, and joins the
@@ -65,11 +72,13 @@ typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;   // tokens of a wave's step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -3e38f;      // the reference of a row that has seen nothing
-constexpr float kSlack = 10.0f;       // how far (log2) a score may pass the reference
-constexpr int kNoLevel = -64;         // no value seen yet
-constexpr int kMaxLevel = 16;         // of a binary16 scale
+// log2 of products of weights and scales: what the reference puts the largest at; and
+// how far it may rise (65504 is binary16's largest).
+constexpr float kLift = 5.0f, kTop = 15.9f;
+constexpr float kDrop = 8.0f;         // how far (log2) a step's largest score may fall
+constexpr float kRoom = 80.0f;        // log2 of the most that a falling reference may make of the weights' sum
+constexpr int kLeastExponent = -24;   // of a scale, 0 too: the smallest of binary16 is 2^-24
 constexpr float kLarge = 0x1p23f;     // references from here on are coarser than a score's difference to them may be
-constexpr int kLift = 3;              // log2 of the weight at the reference of the largest scale
 
 struct Attend {
     KvCache c;
@@ -407,6 +416,17 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
+// The largest of a row's four lanes, which lie 16 apart.
+__device__ __forceinline__ float row_most(float v) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    const uint32_t p0 = p[0], p1 = p[1];   // (a cast of an element itself would take the first)
+    const uint32_t b = __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, p0), __builtin_bit_cast(float, p1)));
+    const auto q = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t q0 = q[0], q1 = q[1];
+    return fmaxf(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
+}
+
 // Waits until at most N loads are under way (older ones have landed), and until
 // what was read from LDS has arrived.
 template <int N>
@@ -551,11 +571,12 @@ __device__ __forceinline__ void stage_queries(const Attend& a, S& sh, uint4 (*q)
 // row's factor they are log2 of weights.
 template <int NB, int QT, bool FULL>
 struct Rows {
-    float factor[QT], m[QT], l[QT];
+    float factor[QT], ref[QT], l[QT];
     int see_lo[QT], see_hi[QT];      // visible tokens
     v4f o[QT][2 * NB];               // sums of dims 16 d + 4 g + i, d the second index
-    float lift[QT];                  // e - kLift, 2^e: what the values' scales the row has seen stay below, but for a factor of 4
-    int low;                         // the least e of the rows; kNoLevel: every step is one with care
+    float drop[QT];                  // a step's largest score less the reference, below which that falls
+    int exponent;                    // steps with scales of 2^exponent and more are looked at; so is every step
+    bool always;                     // where a reference is large
     int all_lo, all_hi, any_lo, any_hi;   // tokens that every row sees, that some row sees
 
     // Rows first .. first + live - 1 (token * group + head of the group) of the sequence.
@@ -566,16 +587,17 @@ struct Rows {
         all_lo = uniform(a.q.window ? t1 - a.q.window + 1 : 0);
         any_lo = uniform(a.q.window ? t0 - a.q.window + 1 : 0);
         any_hi = uniform(t1 < cap ? t1 : cap);
-        low = kNoLevel;
+        exponent = kLeastExponent;
+        always = false;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             const int row = 16 * t + col, pos = sq.pos0 + (first + (row < live ? row : 0)) / group;
             factor[t] = factors[row];
             see_hi[t] = row < live ? (pos < cap ? pos : cap) : -1;
             see_lo[t] = a.q.window ? pos - a.q.window + 1 : 0;
-            m[t] = kFloor;
+            ref[t] = kFloor;
             l[t] = 0.0f;
-            lift[t] = (float)(kNoLevel - kLift);
+            drop[t] = -INFINITY;
 #pragma unroll
             for (int d = 0; d < 2 * NB; ++d) o[t][d] = v4f{0, 0, 0, 0};
         }
@@ -638,62 +660,67 @@ struct Rows {
         v2u16 lv = __builtin_bit_cast(v2u16, levels[0]);
         if constexpr (N > 1) lv = __builtin_elementwise_max(lv, __builtin_bit_cast(v2u16, levels[1]));
         const int bits = lv[0] > lv[1] ? lv[0] : lv[1];
-        bool move = ((bits >> 10) - 14 > low + 2) | (bits >= 0x7C00);
+        bool move = ((bits >> 10) - 14 > exponent) | (bits >= 0x7C00);
+        const float rise = kTop - (float)exponent;
+        uint64_t fall = 0;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             top[t] = fmaxf(sc[t][0], sc[t][1]);
 #pragma unroll
             for (int i = 2; i < 8; ++i) top[t] = fmaxf(top[t], sc[t][i]);
-            move |= top[t] * factor[t] > m[t] + kSlack;
+            const float w = __builtin_fmaf(top[t], factor[t], -ref[t]);
+            move |= w > rise;
+            uint64_t below = __builtin_amdgcn_ballot_w64(w < drop[t]);   // in all four lanes of a row
+            below &= below >> 32;
+            fall |= below & below >> 16 & 0xFFFF;
         }
-        return uniform(__builtin_amdgcn_ballot_w64(move) != 0) != 0;
+        return always | (uniform((__builtin_amdgcn_ballot_w64(move) | fall) != 0) != 0);
     }
 
-    // Moves the references, once in a while: e to a row's largest visible scale
-    // of the step (vs, the lane's), m to its largest score, and what the sums hold
-    // with them.  By row: a token that only later rows see leaves a row's bits
-    // alone, whatever its scale.
+    // Moves the references, once in a while, and with them what the sums hold.  What
+    // is done to a row goes by the scores and scales of the tokens that it sees,
+    // whatever brought the wave here: a token that only other rows see leaves a
+    // row's bits alone.  top: the lane's largest scores; vs: its scales.
     __device__ __forceinline__ void shift(const float (&top)[QT], const float (&sc)[QT][8], const uint32_t (&vs)[2][2 * NB]) {
-        float largest[8];
+        float e[8], most = (float)kLeastExponent;   // of the tokens' largest scales
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            largest[i] = 0.0f;
+            float largest = 0.0f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const float d = fabsf((float)scale_of(vs[i >> 2], i & 3, b));
-                largest[i] = d < INFINITY ? fmaxf(largest[i], d) : largest[i];
+                largest = d < INFINITY ? fmaxf(largest, d) : largest;
             }
+            e[i] = largest > 0.0f ? (float)__builtin_amdgcn_frexp_expf(largest) : (float)kLeastExponent;
+            most = fmaxf(most, e[i]);
         }
-        int least = kMaxLevel;
+        exponent = uniform((int)row_most(most));
+        if (exponent < -14) exponent = -14;   // as look() takes subnormals
+        bool large = false;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            float x = top[t], d = -1.0f;   // (no token)
+            float y = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d = sc[t][i] != -INFINITY ? fmaxf(d, largest[i]) : d;
-#pragma unroll
-            for (int o = 16; o < 64; o <<= 1) {
-                x = fmaxf(x, __shfl_xor(x, o));
-                d = fmaxf(d, __shfl_xor(d, o));
-            }
-            x *= factor[t];
-            const int e = d >= 0x1p-14f ? __builtin_amdgcn_frexp_expf(d) : -14, level = (int)lift[t] + kLift;
-            const int now = d >= 0.0f && (e > level + 2 || level == kNoLevel) ? e : level;
-            const float to = x > m[t] + kSlack ? x : m[t];
-            const float f = __builtin_amdgcn_exp2f(m[t] - to + (float)(level - now));
-            m[t] = to;
-            lift[t] = (float)(now - kLift);
+            for (int i = 0; i < 8; ++i) y = fmaxf(y, __builtin_fmaf(sc[t][i], factor[t], e[i]));
+            y = row_most(y);
+            const float raw = row_most(top[t]), sum = row_most(l[t]), x = raw * factor[t];
+            const float w = __builtin_fmaf(raw, factor[t], -ref[t]);
+            const bool up = (y - ref[t] > kTop) | ((fabsf(ref[t]) >= kLarge) & (x > ref[t]));
+            const bool down = (w < drop[t]) & (x > -INFINITY);
+            // a large reference is a score's own, so that differences to it are exact
+            const float want = fabsf(x) >= kLarge ? x : y - kLift;
+            const float room = fminf(kRoom - (float)__builtin_amdgcn_frexp_expf(sum), 100.0f);
+            const float least = up ? -INFINITY : ref[t] - (room > 0.0f ? room : 0.0f);
+            const float to = up | down ? fmaxf(want, least) : ref[t];
+            drop[t] = up | down ? (to > want ? -INFINITY : x - kDrop - to) : drop[t];
+            const float f = __builtin_amdgcn_exp2f(ref[t] - to);
+            ref[t] = to;
             l[t] *= f;
 #pragma unroll
-            for (int d2 = 0; d2 < 2 * NB; ++d2) this->o[t][d2] *= f;
-            least = see_hi[t] >= 0 && now < least ? now : least;
-            least = fabsf(to) >= kLarge && to != kFloor ? kNoLevel : least;
+            for (int d = 0; d < 2 * NB; ++d) o[t][d] *= f;
+            large |= (fabsf(to) >= kLarge) & (to != kFloor);
         }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-            const int other = __shfl_xor(least, o);
-            least = other < least ? other : least;
-        }
-        low = uniform(least);
+        always = uniform(__builtin_amdgcn_ballot_w64(large) != 0) != 0;
     }
 
     // CAREFUL: where the reference is large, the score is rounded before the
@@ -704,11 +731,10 @@ struct Rows {
 #pragma clang fp contract(off)
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            const float ref = m[t] + lift[t];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float d = __builtin_fmaf(sc[t][i], factor[t], -ref);
-                if (CAREFUL) d = fabsf(m[t]) >= kLarge ? sc[t][i] * factor[t] - m[t] - lift[t] : d;
+                float d = __builtin_fmaf(sc[t][i], factor[t], -ref[t]);
+                if (CAREFUL) d = fabsf(ref[t]) >= kLarge ? sc[t][i] * factor[t] - ref[t] : d;
                 sc[t][i] = __builtin_amdgcn_exp2f(d);
                 l[t] += sc[t][i];
             }
@@ -891,8 +917,8 @@ __device__ __forceinline__ void piece(const Attend& a, Shared<Q4, NB, F, FULL>& 
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (g == 0) {
-            sh.m[wave][16 * t + col] = rows.m[t];
-            sh.l[wave][16 * t + col] = l * __builtin_amdgcn_exp2f(rows.lift[t]);
+            sh.m[wave][16 * t + col] = rows.ref[t];
+            sh.l[wave][16 * t + col] = l;
         }
     }
     __syncthreads();   // and all waves are done with the queries
@@ -902,7 +928,7 @@ __device__ __forceinline__ void piece(const Attend& a, Shared<Q4, NB, F, FULL>& 
         float top = sh.m[0][16 * t + col];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh.m[w][16 * t + col]);
-        const float f = __builtin_amdgcn_exp2f(rows.m[t] - top + rows.lift[t]);
+        const float f = __builtin_amdgcn_exp2f(rows.ref[t] - top);
         if (t > 0) __syncthreads();
 #pragma unroll
         for (int d = 0; d < 2 * NB; ++d)
@@ -1062,10 +1088,9 @@ __device__ __forceinline__ void tall_piece(const Attend& a, Shared<Q4, NB, F, FU
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (row >= mine) continue;
-        const float f = __builtin_amdgcn_exp2f(rows.lift[t]);
 #pragma unroll
         for (int d = 0; d < 2 * NB; ++d)
-            put(a, sq, h, first, own + row, part, kRows, D, 16 * d + 4 * g, rows.o[t][d] * f, rows.m[t], l * f);
+            put(a, sq, h, first, own + row, part, kRows, D, 16 * d + 4 * g, rows.o[t][d], rows.ref[t], l);
     }
 }
 
