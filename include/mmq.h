@@ -660,7 +660,8 @@ int kv_read(const kv_cache *cache, const kv_plan *plan, void *k, void *v, int ha
  * prompt are all meant.
  *
  * Sums, scores and the softmax are float32; codes and binary16 queries enter the
- * products exactly, float32 queries with 22 bits.  Weights times their scales
+ * products exactly, float32 queries with 22 bits and 2^-39 of the head's largest
+ * value at least.  Weights times their scales
  * are rounded to binary16 (relative 2^-11) before they meet the values' codes
  * where q and out are both binary16, else to 22 bits; either way absolutely by
  * 2^-21 of the largest weight among the token's 32 neighbours (of 32 from a

@@ -546,7 +546,8 @@ __device__ __forceinline__ void stage_queries(const Attend& a, S& sh, uint4 (*q)
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-        const int e = amax > 0.0f && amax < INFINITY ? __builtin_amdgcn_frexp_expf(amax) : 14;
+        int e = amax > 0.0f && amax < INFINITY ? __builtin_amdgcn_frexp_expf(amax) : 14;
+        if (a.q.q_half) e = e < 14 ? e : 14;   // binary16 has them as they are; scaled down, subnormals would lose bits
         if ((tid & 15) == 0) sh.factor[row] = fmaxf(ldexpf(size, e - 14), 0x1p-126f);   // not 0: hidden scores stay -inf
 #pragma unroll
         for (int c = 0; c < (NB + 3) / 4; ++c) {

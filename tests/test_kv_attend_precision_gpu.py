@@ -1,6 +1,7 @@
 """Attention over the cache where few tokens have nearly all of the weight and
-the others nearly all of the output: what a product of weight and scale loses
-goes by the tokens next to it, not by the largest weight of the row."""
+the others nearly all of the output (what a product of weight and scale loses
+goes by the tokens next to it, not by the largest weight of the row), and queries
+whose smallest values count."""
 import numpy as np
 import pytest
 import torch
@@ -22,6 +23,7 @@ def put(c, t, k, k_scale, v, v_scale):
     rec = c.data[c.table[0, t // c.page], 0]
     for code, scale, at, place, whole in ((k, k_scale, 0, refs.key_place(dim), c.k), (v, v_scale, 2, refs.value_place(dim), c.v)):
         d = np.float16(scale)
+        assert np.abs(code).max() <= (127 if bits == 8 else 7)
         rec[parts[at] + t % c.page * cb:][:cb] = refs.code_bytes(code, place, bits, at == 0)
         rec[parts[at + 1] + t % c.page * sb:][:sb] = np.full(dim // 32, d).view(np.uint8)
         whole[0][0, t] = code * np.float64(d)
@@ -147,3 +149,22 @@ def test_peaked_scores_beside_scales_of_any_size(group, half, spread):
     """Random keys, values and scales, with scores up to some hundred: a row's
     largest products move from token to token."""
     Case(83, 1, group, 64, 64, 8, [900, 260], [1, 1], half, spread=spread).both(most=1)
+
+
+@pytest.mark.parametrize("group", [1, 40, 200])
+@pytest.mark.parametrize("out_half", [False, True])
+@pytest.mark.parametrize("large", [8192.0, 16384.0, 32768.0, 65504.0])
+@pytest.mark.parametrize("small", [1, 3, 1023])
+def test_binary16_queries_are_exact(group, out_half, large, small):
+    """Scores that the smallest values of a head make beside its largest one."""
+    c = Case(84, 1, group, 32, 16, 8, [3], [1], True)
+    c.q[0].reshape(group, 32)[:, :] = 0
+    c.q[0].reshape(group, 32)[:, 0] = large
+    c.q[0].reshape(group, 32)[:, 1] = small * 2.0 ** -24
+    for t, code in enumerate((127, 0, -127)):
+        k = np.zeros(32, np.int64)
+        k[1] = code
+        put(c, t, k, 1 / 64, np.arange(32) + 45 * t, 1 / 64)
+    out, lse = c.run(0, 2.0 ** 24 / small, f16=out_half)
+    torch.cuda.synchronize()
+    c.check(out, lse, scale=2.0 ** 24 / small, half=out_half)
