@@ -1198,30 +1198,31 @@ __global__ __launch_bounds__(64 * waves_of(F),
 }
 
 template <bool Q4, int NB, Form F>
-void launch_form(const Attend& a, dim3 grid, hipStream_t stream) {
+hipError_t launch_form(const Attend& a, dim3 grid, hipStream_t stream) {
     if (a.q.q_half && a.q.out_half) {   // else the query or the output has more bits than binary16
         hipLaunchKernelGGL((attend_kernel<Q4, NB, F, false>), grid, dim3(64 * waves_of(F)), 0, stream, a);
     } else if constexpr (fits(Q4, NB, F, true)) {
         hipLaunchKernelGGL((attend_kernel<Q4, NB, F, true>), grid, dim3(64 * waves_of(F)), 0, stream, a);
+    } else {
+        return hipErrorInvalidConfiguration;   // not built
     }
+    return hipGetLastError();
 }
 
 template <bool Q4, int LO, int HI>
 hipError_t launch_dims(const Attend& a, Form f, dim3 grid, hipStream_t stream) {
+    // cut() takes these without a look at fits()
+    static_assert(fits(Q4, LO, kNarrow, true) && fits(Q4, LO, kTall, true) && (!has_wide(Q4, LO) || fits(Q4, LO, kWide, true)));
     if constexpr (LO < HI) {
         if (a.c.dim > 32 * LO) return launch_dims<Q4, LO + 1, HI>(a, f, grid, stream);
     }
-    switch (f) {
-        case kNarrow: launch_form<Q4, LO, kNarrow>(a, grid, stream); break;
-        case kWide:
-            if constexpr (has_wide(Q4, LO)) launch_form<Q4, LO, kWide>(a, grid, stream);
-            break;
-        case kWide8:
-            if constexpr (has_wide(Q4, LO)) launch_form<Q4, LO, kWide8>(a, grid, stream);
-            break;
-        case kTall: launch_form<Q4, LO, kTall>(a, grid, stream); break;
+    if (f == kNarrow) return launch_form<Q4, LO, kNarrow>(a, grid, stream);
+    if (f == kTall) return launch_form<Q4, LO, kTall>(a, grid, stream);
+    if constexpr (has_wide(Q4, LO)) {
+        if (f == kWide) return launch_form<Q4, LO, kWide>(a, grid, stream);
+        if (f == kWide8) return launch_form<Q4, LO, kWide8>(a, grid, stream);
     }
-    return hipGetLastError();
+    return hipErrorInvalidConfiguration;   // not built
 }
 
 // Head sizes up to 128, and above: each in a file of its own, to build side by side.
