@@ -16,8 +16,10 @@ namespace {
 
 constexpr int kMaxPairs = 512;
 
+// Rows, and so runs of 8, lie on 16-byte boundaries, float32 too: what is promised
+// to the compiler is no more.
 template <typename T, int N>
-struct alignas(N * sizeof(T)) Vec {
+struct alignas(16) Vec {
     T v[N];
 };
 
@@ -34,6 +36,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Rope rope, HeadRows x, HeadRo
         // Pieces of 8 values: first halves (with their partners) or whole
         // pairs, then what is not rotated.
         typedef Vec<T, 8> V;
+        static_assert(alignof(V) == 16 && sizeof(V) == 8 * sizeof(T));
         const int turned = (rope.adjacent ? 2 * pairs : pairs) >> 3, per = turned + (rest >> 3);
         for (int i = threadIdx.x; i < heads * per; i += blockDim.x) {
             const int h = i / per, c = i - h * per;

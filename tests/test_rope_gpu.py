@@ -74,6 +74,22 @@ def test_strides(half):
         assert torch.equal(x, want) and torch.equal(wide[:, heads * dim:], before[:, heads * dim:])
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_rows_on_16_byte_boundaries_alone(adjacent):
+    """Float32 rows that begin 16 bytes past a 32-byte boundary, and at a stride
+    of an odd number of 16 bytes."""
+    rng = np.random.default_rng(14)
+    n, heads, dim, pairs = 6, 2, 48, 16
+    flat = to_dev(rng.standard_normal(4 + n * (heads * dim + 4)).astype(np.float32))
+    x = flat[4:].view(n, heads * dim + 4)[:, :heads * dim]
+    assert x.data_ptr() % 32 == 16 and x.stride(0) % 8 == 4
+    pos, f = to_dev(rng.integers(0, 5000, n).astype(np.int32)), to_dev(_freq(pairs))
+    was = x.cpu().numpy().copy()
+    b.rope(x, heads, b.Rope(pos, f, None, adjacent), out=x)
+    torch.cuda.synchronize()
+    _check(x.cpu().numpy(), was, refs.rope(was, heads, pos.cpu().numpy(), f.cpu().numpy(), adjacent=adjacent), False, "rope")
+
+
 def test_non_finite_values_stay_in_their_pair():
     x = torch.ones(2, 64, device="cuda:0")
     x[0, 5], x[1, 40] = float("nan"), float("inf")
