@@ -664,10 +664,9 @@ int kv_read(const kv_cache *cache, const kv_plan *plan, void *k, void *v, int ha
  * value at least.  Weights times their scales
  * are rounded to binary16 (relative 2^-11) before they meet the values' codes
  * where q and out are both binary16, else to 22 bits; either way absolutely by
- * 2^-21 of the largest weight among the token's 32 neighbours (of 32 from a
- * multiple of 32 on) times the largest value that the row has seen, for tokens down to 2^-40
- * of the row's largest weight.  Equal calls give equal bits, but the order of a
- * sum may depend on the lengths of all sequences.
+ * 2^-29 of the largest product of a weight and its token's largest value that
+ * the row has met.  Equal calls give equal bits, but the order of a sum may depend
+ * on the lengths of all sequences.
  *
  *   most      : an upper bound of any sequence's rows in this call; rows past it
  *               are left as they were.

@@ -27,15 +27,16 @@
 //
 // The softmax keeps a running reference r per row; sums and weights are of
 // exp2(s - r).  What binary16 has to hold is a weight times its value's scale, so
-// r goes by the largest such product of a step: it is put 2^5 below that, and moves
-// (everything so far is rescaled) only when a product may pass binary16's range,
-// or when the step's largest score is 2^8 below that of the step that set it.
-// Few steps do either: those leave the inner loop.  Products lose bits below
-// 2^-14, by 2^-25 absolutely: 2^-21 of the step's largest weight times the
-// largest value that the row has seen, whatever far larger weight (of a first token
-// whose values are small, say) came before.  1200 tokens that share 2^-17 of the weight
-// beside one without a value: 3e-7 off in float32, 4% with a reference that only rises
-// with the scores (level in time but for some steps more: prompt chunk 513 and 516 us).
+// r goes by the largest such product: it is put 2^5 below that of the first step, and
+// moves (everything so far is rescaled) only when a product may pass binary16's
+// range, which few steps do: those leave the inner loop.  Products lose bits below
+// 2^-14, by 2^-25 absolutely: 2^-30 of the largest so far, of which a code's step is 2^-8
+// or 2^-4.  Weights alone do not tell: beside a first token that has nearly all of the
+// weight but a small value the others make the output.  1200 tokens that share 2^-17 of
+// the weight beside one without a value: 3e-7 off in float32, 4% with a reference that
+// goes by the scores.  A reference that also falls where a step's scores are 2^8 (2^20)
+// lower takes 1125 (716) us for 603, a prompt chunk whose scores spread (standard
+// deviation 5).
 //
 // Few rows (kNarrow, kWide) are bound by the cache: every wave has its own steps,
 // copied straight into LDS while the step before is worked on, and joins the
@@ -72,12 +73,10 @@ typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;   // tokens of a wave's step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -3e38f;      // the reference of a row that has seen nothing
-// log2 of products of weights and scales: what the reference puts the largest at; and
+// log2 of products of weights and scales: what the reference puts the largest at, and
 // how far it may rise (65504 is binary16's largest).
 constexpr float kLift = 5.0f, kTop = 15.9f;
-constexpr float kDrop = 8.0f;         // how far (log2) a step's largest score may fall
-constexpr float kRoom = 80.0f;        // log2 of the most that a falling reference may make of the weights' sum
-constexpr int kLeastExponent = -24;   // of a scale, 0 too: the smallest of binary16 is 2^-24
+constexpr float kNoScale = -64.0f;    // what counts as the exponent of a scale of 0 (the smallest other is 2^-24)
 constexpr float kLarge = 0x1p23f;     // references from here on are coarser than a score's difference to them may be
 
 struct Attend {
@@ -575,7 +574,6 @@ struct Rows {
     float factor[QT], ref[QT], l[QT];
     int see_lo[QT], see_hi[QT];      // visible tokens
     v4f o[QT][2 * NB];               // sums of dims 16 d + 4 g + i, d the second index
-    float drop[QT];                  // a step's largest score less the reference, below which that falls
     int exponent;                    // steps with scales of 2^exponent and more are looked at; so is every step
     bool always;                     // where a reference is large
     int all_lo, all_hi, any_lo, any_hi;   // tokens that every row sees, that some row sees
@@ -588,7 +586,7 @@ struct Rows {
         all_lo = uniform(a.q.window ? t1 - a.q.window + 1 : 0);
         any_lo = uniform(a.q.window ? t0 - a.q.window + 1 : 0);
         any_hi = uniform(t1 < cap ? t1 : cap);
-        exponent = kLeastExponent;
+        exponent = -24;
         always = false;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
@@ -598,7 +596,6 @@ struct Rows {
             see_lo[t] = a.q.window ? pos - a.q.window + 1 : 0;
             ref[t] = kFloor;
             l[t] = 0.0f;
-            drop[t] = -INFINITY;
 #pragma unroll
             for (int d = 0; d < 2 * NB; ++d) o[t][d] = v4f{0, 0, 0, 0};
         }
@@ -663,19 +660,14 @@ struct Rows {
         const int bits = lv[0] > lv[1] ? lv[0] : lv[1];
         bool move = ((bits >> 10) - 14 > exponent) | (bits >= 0x7C00);
         const float rise = kTop - (float)exponent;
-        uint64_t fall = 0;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             top[t] = fmaxf(sc[t][0], sc[t][1]);
 #pragma unroll
             for (int i = 2; i < 8; ++i) top[t] = fmaxf(top[t], sc[t][i]);
-            const float w = __builtin_fmaf(top[t], factor[t], -ref[t]);
-            move |= w > rise;
-            uint64_t below = __builtin_amdgcn_ballot_w64(w < drop[t]);   // in all four lanes of a row
-            below &= below >> 32;
-            fall |= below & below >> 16 & 0xFFFF;
+            move |= __builtin_fmaf(top[t], factor[t], -ref[t]) > rise;
         }
-        return always | (uniform((__builtin_amdgcn_ballot_w64(move) | fall) != 0) != 0);
+        return always | (uniform(__builtin_amdgcn_ballot_w64(move) != 0) != 0);
     }
 
     // Moves the references, once in a while, and with them what the sums hold.  What
@@ -683,7 +675,7 @@ struct Rows {
     // whatever brought the wave here: a token that only other rows see leaves a
     // row's bits alone.  top: the lane's largest scores; vs: its scales.
     __device__ __forceinline__ void shift(const float (&top)[QT], const float (&sc)[QT][8], const uint32_t (&vs)[2][2 * NB]) {
-        float e[8], most = (float)kLeastExponent;   // of the tokens' largest scales
+        float e[8], most = -14.0f;   // exponents of the tokens' largest scales; look() takes subnormals for 2^-14
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float largest = 0.0f;
@@ -692,11 +684,10 @@ struct Rows {
                 const float d = fabsf((float)scale_of(vs[i >> 2], i & 3, b));
                 largest = d < INFINITY ? fmaxf(largest, d) : largest;
             }
-            e[i] = largest > 0.0f ? (float)__builtin_amdgcn_frexp_expf(largest) : (float)kLeastExponent;
+            e[i] = largest > 0.0f ? (float)__builtin_amdgcn_frexp_expf(largest) : kNoScale;
             most = fmaxf(most, e[i]);
         }
         exponent = uniform((int)row_most(most));
-        if (exponent < -14) exponent = -14;   // as look() takes subnormals
         bool large = false;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
@@ -704,16 +695,10 @@ struct Rows {
 #pragma unroll
             for (int i = 0; i < 8; ++i) y = fmaxf(y, __builtin_fmaf(sc[t][i], factor[t], e[i]));
             y = row_most(y);
-            const float raw = row_most(top[t]), sum = row_most(l[t]), x = raw * factor[t];
-            const float w = __builtin_fmaf(raw, factor[t], -ref[t]);
+            const float x = row_most(top[t]) * factor[t];
             const bool up = (y - ref[t] > kTop) | ((fabsf(ref[t]) >= kLarge) & (x > ref[t]));
-            const bool down = (w < drop[t]) & (x > -INFINITY);
             // a large reference is a score's own, so that differences to it are exact
-            const float want = fabsf(x) >= kLarge ? x : y - kLift;
-            const float room = fminf(kRoom - (float)__builtin_amdgcn_frexp_expf(sum), 100.0f);
-            const float least = up ? -INFINITY : ref[t] - (room > 0.0f ? room : 0.0f);
-            const float to = up | down ? fmaxf(want, least) : ref[t];
-            drop[t] = up | down ? (to > want ? -INFINITY : x - kDrop - to) : drop[t];
+            const float to = up ? (fabsf(x) >= kLarge ? x : y - kLift) : ref[t];
             const float f = __builtin_amdgcn_exp2f(ref[t] - to);
             ref[t] = to;
             l[t] *= f;
