@@ -110,14 +110,15 @@ Cut cut(const KvCache& c, const KvPlan& p, const KvQuery& q) {
     // kWide's tiles are of 32) kTall, whose waves share the codes' way to operands;
     // below, it has idle waves, but of 96 and 128 dims codes are most of the work: of
     // 128 in 8 bits always, else while tiles are few (kTall / kWide, us, 8 heads, 2048
-    // tokens: 128 dims, 8 bits, 32 rows of 32 sequences 77 / 90, in float32 112 / 116, 96
-    // rows 113 / 135 and 144 / 187; 4 bits, 32 rows of 2 sequences 28 / 35, in float32 29 /
-    // 38, of 32 78 / 72 and 110 / 92; 64 dims, of 32 53 / 40; 256 dims, 64 rows 157 / 144,
-    // 96 rows 185 / 210).  Of kWide's workgroups
-    // those of 8 waves where there are no more tiles than CUs, else of 4, whose beginnings
-    // and ends overlap (8 / 4 waves, us, 8 heads of 128, 32 rows: 16 sequences of 2048
-    // tokens 65 / 70, 32 86 / 92, 64 167 / 138; of 64, 48 rows: 16 windows of 1024 25 /
-    // 30, 64 sequences of 1024 49 / 37).
+    // tokens: 128 dims, 8 bits, 32 rows of 32 sequences 72 / 82, in float32 106 / 103, 96
+    // rows 107 / 121 and 135 / 163; 4 bits, 32 rows of 2 sequences 26 / 27, of 8 42 / 45, in
+    // float32 29 / 30 and 42 / 53, of 32 69 / 66 and 102 / 90; 96 dims, 8 bits, of 2 24 /
+    // 24, of 8 37 / 35, in float32 27 / 26 and 39 / 42; 64 dims, of 32 50 / 40, 124 rows 72
+    // / 56, 128 71 / 56 but of 2 27 / 34; 256 dims, 64 rows 151 / 136, 65 175 / 198).  Of
+    // kWide's workgroups those of 8 waves where there are no more tiles than CUs, else
+    // of 4, whose beginnings and ends overlap (8 / 4 waves, us, 8 heads of 128, 4 bits, 32
+    // rows: 16 sequences of 2048 tokens 49 / 52, 32 61 / 66, 64 108 / 97; of 64, 48 rows: 16
+    // windows of 1024 26 / 30, 64 sequences of 1024 49 / 37).
     const bool codes = !has_wide(c.q4, nb) || ((nb == 3 || nb == 4) && c.heads * (int64_t)p.seqs <= kCus / 4);
     int64_t all = form(rows <= 16 ? kNarrow : rows < (nb > 4 ? 65 : codes ? 17 : 128) ? kWide : kTall);
     if (r.form == kWide && all <= kCus && fits(c.q4, nb, kWide8, full)) all = form(kWide8);
@@ -125,20 +126,25 @@ Cut cut(const KvCache& c, const KvPlan& p, const KvQuery& q) {
     // Splitting takes steps off the longest sequence's and spreads them over idle
     // CUs; the second launch and the parts' way through memory cost what 2 to 5 of
     // a workgroup's steps do.  Not split, us, against split, caches from HBM, 8 heads
-    // of 128 with 4 query heads each: 1 sequence of 512 tokens 12.1 / 12.7, of 768 14.7
-    // / 13.0, of 1024 17.1 / 12.6; 16 of 1024 18.7 / 22.5, of 2048 29.1 / 28.4; 64 of
-    // 1024 33.6 / 36.7; with 32 rows 1 of 256 24.1 / 29.0, of 768 34.7 / 30.9, 16 of 768
-    // 47.8 / 50.2, of 2048 78 / 65; 600 rows of 4 over 1024 60 / 72, over 2048 106 / 92;
-    // 8 heads of 256, 4 rows: 1 of 256 15.7 / 16.3, of 512 22.3 / 16.6.  Not past 1280
-    // tokens, as the host does not know how ragged the lengths are; but also
-    // where tiles of one sequence fill the chip, whose last ones see most and go
-    // first (1500 rows of 4, 376 tiles, over 2048 126 / 145, over 4096 245 / 231).
+    // of 128 with 4 query heads each: 1 sequence of 512 tokens 11.7 / 12.4, of 768 15.0
+    // / 13.2, of 1024 17.4 / 12.9; 16 of 1024 18.8 / 22.1, of 2048 29.0 / 28.4; 64 of
+    // 1024 33.1 / 36.6; with 32 rows 1 of 256 20.2 / 22.4, of 768 39.9 / 24.0, 16 of 768
+    // 42.6 / 41.1, of 2048 90 / 53; 600 rows of 4 over 1024 60 / 77, over 2048 106 / 98;
+    // 8 heads of 256, 4 rows: 1 of 256 13.4 / 15.5, of 512 19.9 / 16.4.  Not past 1280
+    // tokens, as the host does not know how ragged the lengths are; but also where
+    // one sequence is all there is and its tiles fill the chip, as its last ones see
+    // most and go first (1500 rows of 4, 376 tiles, over 2048 129 / 164, over 4096 249 /
+    // 251; 2048, 512 tiles, over 2048 143 / 148, over 8192 505 / 509; 4096 over 4096 438 /
+    // 517).  Of more sequences equal ones would be level (4 of 512 rows over 2048 145 / 152,
+    // over 8192 508 / 512; 16 of 130 over 4096 472 / 363), but a long history among
+    // them would be one workgroup's a tile (63 decoding sequences of 4000 tokens and a chunk of
+    // 512 2617 us, 323 cut).
     int64_t span = (int64_t)p.width << c.shift;
     if (q.window && q.window < span - q.most - kTile) span = q.window + (int64_t)q.most + kTile;
     const int unit = unit_of(r.form);
     const int64_t units = (span + unit - 1) / unit, idle = all < kCus ? kCus - all : 0;
     const int worth = r.form == kWide8 ? (c.dim > 64 ? 2 : 3) : c.dim > 128 ? 3 : 5;
-    const bool direct = (span <= 1280 && units * idle <= worth * kCus) || (r.tiles > 1 && all >= 2 * kCus);
+    const bool direct = (span <= 1280 && units * idle <= worth * kCus) || (p.seqs == 1 && r.tiles > 1 && all >= 2 * kCus);
     r.wgs = direct ? 0 : runs;
     r.many = runs > 16 * all;
     r.joined = !direct;

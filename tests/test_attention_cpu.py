@@ -182,3 +182,17 @@ def test_layout_reference_round_trip(dim, bits):
         code = rng.integers(-7, 8, dim)
         got = refs.code_bytes(code, place, bits, key)
         assert got.shape == (dim * bits // 8,) and np.array_equal(refs.byte_codes(got, place, bits, key), code)
+
+
+@pytest.mark.parametrize("seqs,n,most,width,cut", [
+    (1, 2048, 2048, 100, False), (1, 2048, 2048, 1 << 14, False),   # one sequence's tiles fill the chip
+    (64, 575, 512, 100, True), (4, 515, 512, 2048, True), (8, 4096, 512, 2048, True), (64, 64, 64, 64, True),   # of several
+    (1, 512, 512, 100, True), (64, 64, 1, 16, False), (1, 1, 1, 16, True)])
+def test_what_is_cut(lib, seqs, n, most, width, cut):
+    """8 heads of 128 with 4 query heads each: several sequences on a table past
+    1280 tokens are cut, however many tiles they may have, as their lengths may differ."""
+    c = cache(pages=1 << 20, heads=8, head_dim=128, page=64, data=0)
+    size = ctypes.c_int64(-1)
+    q = query(n=n, most=most, heads=32, q_half=1, out_half=1)
+    assert lib.kv_attend_workspace(c, plan(seqs=seqs, width=width), q, size) == OK
+    assert (size.value > 0) == cut

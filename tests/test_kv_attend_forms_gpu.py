@@ -47,19 +47,15 @@ def check_some(c, out, lse, s, rows, window=0):
 
 @pytest.mark.parametrize("half,bits,window", [(True, 8, 0), (False, 4, 0), (True, 4, 700)])
 def test_prompt_uncut_past_short_contexts(half, bits, window):
-    """Tiles that fill the chip go uncut on a table of any length: a long prompt,
-    and sequences with few rows beside it."""
-    c = Case(101, 12, 1, 32, 64, bits, [2150, 40, 1500], [2050, 1, 130], half)
-    most = 2050
-    assert c.table.shape[1] * c.page > 1280 and workspace(c, most, window) == 0
+    """One sequence's tiles that fill the chip go uncut on a table of any length."""
+    c = Case(101, 32, 1, 32, 64, bits, [2150], [2050], half)
+    assert c.table.shape[1] * c.page > 1280 and workspace(c, 2050, window) == 0
     note("uncut prompt half=%d bits=%d window=%d" % (half, bits, window))
-    out, lse = c.run(window, most=most)
+    out, lse = c.run(window, most=2050)
     torch.cuda.synchronize()
     out, lse = out.cpu().numpy(), lse.cpu().numpy()
     assert np.isfinite(out).all() and np.isfinite(lse).all()
     check_some(c, out, lse, 0, [0, 1, 15, 16, 31, 127, 128, 129, 1023, 1919, 1920, 2047, 2048, 2049], window)
-    check_some(c, out, lse, 1, [0], window)
-    check_some(c, out, lse, 2, [0, 15, 16, 127, 128, 129], window)
 
 
 FORMS = [
@@ -120,10 +116,11 @@ def test_hidden_tokens_leave_rows_of_each_form(dim, bits, half, group, new, seqs
         at[:] = was
 
 
-def test_one_long_history_among_many_uncut_tiles():
-    """A chunk whose tiles fill the chip beside a sequence with a long history."""
+def test_tiles_of_several_sequences_are_cut():
+    """A chunk, a long history and a short one in one call: as many tiles as fill the
+    chip, but their lengths may differ, so that they are cut."""
     c = Case(104, 8, 2, 32, 64, 8, [2048, 9000, 5], [2048, 2, 1], True)
-    assert workspace(c, 2048) == 0
+    assert workspace(c, 2048) > 0
     out, lse = c.run(most=2048)
     torch.cuda.synchronize()
     out, lse = out.cpu().numpy(), lse.cpu().numpy()
