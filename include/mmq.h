@@ -576,9 +576,10 @@ int rope_rows(const rope_plan *rope, const void *x, int64_t x_stride, int half, 
  * code * scale of its 32-value block, with
  *   KV_Q8: da = max|x| * r in float32, r = float32(1/127); code = round(x / da),
  *          IEEE division, ties away from zero; int8, -127 .. 127;
- *          scale = binary16(da).  (q8_quantize_rows divides by 127 instead: a da
- *          a float32 step apart at most, so the code of a value within that of a
- *          tie may be its neighbour.)
+ *          scale = binary16(da).  (A step by multiplication, as tensor libraries
+ *          take it on a device: codes are compared with theirs.  q8_quantize_rows
+ *          divides by 127 instead: a da a float32 step apart at most, so the code
+ *          of a value within that of a tie may be its neighbour.)
  *   KV_Q4: the same with float32(1/7), code -7 .. 7, stored as code + 8.
  * A block with a NaN or an infinity gets a NaN scale, and one whose da is past
  * binary16 an infinite one.  Order of a token's codes (nb = head_dim / 32):
@@ -660,23 +661,25 @@ int kv_read(const kv_cache *cache, const kv_plan *plan, void *k, void *v, int ha
  * prompt are all meant.
  *
  * Sums, scores and the softmax are float32; codes and binary16 queries enter the
- * products exactly, float32 queries with 22 bits and 2^-39 of the head's largest
- * value at least.  Weights times their scales
- * are rounded to binary16 (relative 2^-11) before they meet the values' codes
- * where q and out are both binary16, else to 22 bits; either way absolutely by
- * 2^-29 of the largest product of a weight and its token's largest value that
- * the row has met.  Equal calls give equal bits, but the order of a sum may depend
- * on the lengths of all sequences.
+ * products exactly, float32 queries with 22 bits, or to 2^-39 of the head's
+ * largest value.  Weights times their scales are rounded to binary16 (relative
+ * 2^-11) before they meet the values' codes where q and out are both binary16,
+ * else to 22 bits (who keeps binary16 and wants these takes a float32 out and
+ * rounds it); either way absolutely by 2^-29 of the largest product of a weight
+ * and its token's largest value that the row has met.  Equal calls give equal
+ * bits, but the order of a sum may depend on the lengths of all sequences.
  *
  *   most      : an upper bound of any sequence's rows in this call; rows past it
- *               are left as they were.
+ *               are left as they were.  It chooses the kernel, for all sequences:
+ *               the nearer it is, the faster the call.
  *   out       : must not overlap q or the cache.
  *   workspace : kv_attend_workspace's bytes, for this call alone until it has
  *               finished (calls on two streams need two).  MMQ_ERR_SHAPE if it is
  *               smaller.
  * A window of more than 2^30 is none.  MMQ_ERR_SHAPE for heads not a multiple of
- * the cache's, a negative window or most < 1; MMQ_ERR_OVERFLOW for most * heads / cache heads >= 2^28, or steps of
- * 128 tokens of a sequence times its tiles of 16 rows >= 2^31.
+ * the cache's, a negative window or most < 1; MMQ_ERR_OVERFLOW for most * heads /
+ * cache heads >= 2^28, or 2^31 and more steps of 128 tokens of a sequence (and one
+ * more) times tiles of 16 of its rows of a cache head times cache heads.
  */
 typedef struct kv_query {
     const void *q;              /* [n][q_stride], heads * head_dim a row */

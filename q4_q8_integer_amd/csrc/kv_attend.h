@@ -16,8 +16,8 @@
 //                (exact), the weights p * (scale of the value's block) as
 //                binary16 where q and out are (a rounding of 2^-11, as the
 //                output's own: 2.9e-4 from 64 bits where the output's alone is
-//                2.1e-4), else as hi + lo (22 bits).  hi + lo there too takes 723
-//                us for 505 (prompt chunk), 141 for 124 (own heads, 4 bits)
+//                2.1e-4), else as hi + lo (22 bits).  hi + lo there too takes 705
+//                us for 501 (prompt chunk), 137 for 122 (own heads, 4 bits)
 //
 // so all sums are float32.  S^T leaves a lane with 4 keys of each half of its
 // 32, of one row; the second product takes its k index in that order, so
@@ -33,7 +33,7 @@
 // 2^-14, by 2^-25 absolutely: 2^-30 of the largest so far, of which a code's step is 2^-8
 // or 2^-4.  Weights alone do not tell: beside a first token that has nearly all of the
 // weight but a small value the others make the output.  1200 tokens that share 2^-17 of
-// the weight beside one without a value: 3e-7 off in float32, 4% with a reference that
+// the weight beside one without a value: 4e-7 off in float32, 4% with a reference that
 // goes by the scores.  A reference that also falls where a step's scores are 2^8 (2^20)
 // lower takes 1125 (716) us for 603, a prompt chunk whose scores spread (standard
 // deviation 5).
@@ -42,9 +42,9 @@
 // copied straight into LDS while the step before is worked on, and joins the
 // others in LDS at the end.  One token of 32 query heads on 8, 131000 tokens, 8 bits
 // (285 MB): 56 us, 5.1 TB/s, and 7 for the join; 64 ragged sequences up to 8100
-// (539 MB) 117 + 5; 32 sequences of own heads, 4 bits (517 MB) 112 + 5; 16 windows of
-// 1024, 48 rows 28 (latency: 9 steps of a workgroup, 128 workgroups).  Many rows
-// (kTall) are bound by vector issue: 2048 rows of 4 over 6100 tokens before them 498 us,
+// (539 MB) 120 + 5; 32 sequences of own heads, 4 bits (517 MB) 114 + 5; 16 windows of
+// 1024, 48 rows 26 (latency: 9 steps of a workgroup, 128 workgroups).  Many rows
+// (kTall) are bound by vector issue: 2048 rows of 4 over 6100 tokens before them 500 us,
 // 480 TFLOP/s, the vector units busy 67% of the time, the matrix units 19%.  Per
 // 32 keys and 16 rows a wave has 16 matrix instructions of 16 cycles and some 200 vector
 // ones of 4: 32 scales on scores, 32 on weights, 40 of the softmax, the rest copies and
@@ -473,14 +473,15 @@ constexpr bool fits(bool q4, int nb, Form f, bool full) { return lds_bytes(q4, n
 // Workgroups a CU by registers: waves with four tiles of sums, of heads above 128
 // dims, and kTall's with queries of two parts from 96 dims on take more than half of
 // what two of a SIMD share (600 rows of 4 over 3000 tokens, float32, 128 dims: two
-// workgroups with spills 217 us, one 159; 96 dims 139 and 143, but 46 prompts of 33
-// tokens 218 and 171; binary16 with one 732 us where two take 507).
+// workgroups with spills 188 us, one 159, 32 rows of 32 sequences of 2048 140 and 108; 96
+// dims, with fewer spills, 135 and 144; the binary16 chunk with one 714 us where two take
+// 502).
 constexpr int by_registers(int nb, Form f, bool full) {
     return 4 * (f == kNarrow ? 3 : f == kTall && nb <= (full ? 2 : 4) ? 4 : 2) / waves_of(f);
 }
 // Two steps where that leaves as many workgroups a CU (two count as many): with
-// one, one sequence of 131000 tokens takes 71 us instead of 66, 32 of 4096, 4 bits, 125
-// instead of 119; kTall with one is 3 to 5% faster at 64 dims, 4% slower at 256.
+// one, one sequence of 131000 tokens takes 73 us instead of 67, 32 of 4096, 4 bits, 130
+// instead of 123; kTall with one is 1 to 3% faster up to 128 dims, 4% slower at 256.
 constexpr int stages(bool q4, int nb, Form f, bool full) {
     const int want = by_registers(nb, f, full) < 2 || 2 * lds_bytes(q4, nb, f, full, 1) > kLds ? 1 : 2;
     return want * lds_bytes(q4, nb, f, full, 2) <= kLds ? 2 : 1;

@@ -152,7 +152,7 @@ Cut cut(const KvCache& c, const KvPlan& p, const KvQuery& q) {
     r.join_rows = (r.most + per_join - 1) / per_join;
     // Workgroups that find nothing to join take their time too; a look at all runs
     // for those that have is 1 to 2 us (1 sequence of 4096 tokens, 8 heads of 128, 96
-    // rows: 35 us with it, 110 without; own heads of 32 sequences 131 and 123).
+    // rows: 39 us with it, 54 without).
     r.joins = all < runs && (int64_t)runs * r.join_rows > 2048 ? (int)all : runs;
     return r;
 }
