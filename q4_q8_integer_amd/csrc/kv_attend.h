@@ -73,9 +73,9 @@ typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;   // tokens of a wave's step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -3e38f;      // the reference of a row that has seen nothing
-// log2 of products of weights and scales: what the reference puts the largest at, and
-// how far it may rise (65504 is binary16's largest).
-constexpr float kLift = 5.0f, kTop = 15.9f;
+// log2 of products of weights and scales: what the reference puts the largest at,
+// where a step is looked at, and how far a product may rise (65504 is binary16's largest).
+constexpr float kLift = 5.0f, kLook = 15.8f, kTop = 15.9f;
 constexpr float kNoScale = -64.0f;    // what counts as the exponent of a scale of 0 (the smallest other is 2^-24)
 constexpr float kLarge = 0x1p23f;     // references from here on are coarser than a score's difference to them may be
 
@@ -660,7 +660,7 @@ struct Rows {
         if constexpr (N > 1) lv = __builtin_elementwise_max(lv, __builtin_bit_cast(v2u16, levels[1]));
         const int bits = lv[0] > lv[1] ? lv[0] : lv[1];
         bool move = ((bits >> 10) - 14 > exponent) | (bits >= 0x7C00);
-        const float rise = kTop - (float)exponent;
+        const float rise = kLook - (float)exponent;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             top[t] = fmaxf(sc[t][0], sc[t][1]);
@@ -692,6 +692,8 @@ struct Rows {
         bool large = false;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
+            // The largest product.  That of far scores is rounded to their float32 steps, up
+            // to 1/2: one that counts as kTop at most is 2^15.94 then (15.875 and half of 1/8).
             float y = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) y = fmaxf(y, __builtin_fmaf(sc[t][i], factor[t], e[i]));

@@ -160,3 +160,28 @@ def test_binary16_queries_are_exact(group, out_half, large, small):
     out, lse = c.run(0, 2.0 ** 24 / small, f16=out_half)
     torch.cuda.synchronize()
     c.check(out, lse, scale=2.0 ** 24 / small, half=out_half)
+
+
+@pytest.mark.parametrize("base", [1e3, 1e5, 7e5, 1.4e6, 2.8e6, 5.5e6])
+@pytest.mark.parametrize("half", [False, True])
+def test_far_scores_beside_scales_of_any_size(base, half):
+    """Scores whose float32 steps come near those of their differences, over values
+    of 2^-14 to 2^9: what comes out lies among the values."""
+    c = Case(85, 1, 200, 64, 64, 8, [1200], [1], half)
+    rng = np.random.default_rng([85, int(base)])
+    parts, q = refs.record_parts(64, 64, 8), np.zeros((200, 64))
+    q[:, :32] = base / (32 * 127) * (1 + 0.2 * rng.random((200, 1)))
+    q[:, 32] = 0.5 + rng.random(200)
+    c.q[:] = q.reshape(1, -1)
+    for t in range(1200):
+        k = np.full(64, 127, np.int64)
+        k[32:] = 0
+        k[32] = rng.integers(-127, 128)
+        put(c, t, k, 1.0, rng.integers(64, 128, 64), 2.0 ** rng.uniform(-21, 2))
+        c.data[c.table[0, t // 64], 0, parts[1] + t % 64 * 4 + 2:][:2] = np.full(1, 0.1, np.float16).view(np.uint8)
+    out, lse = c.run(0, 1.0)
+    torch.cuda.synchronize()
+    got, v = out.cpu().numpy().reshape(200, 64).astype(np.float64), c.v[0][0]
+    assert np.isfinite(got).all() and torch.isfinite(lse).all()
+    # weights are positive and sum up to 1 but for roundings: 2^-11 each, sums of 1200
+    assert (got <= v.max(0) * (1 + 2.0 ** -9)).all() and (got >= v.min(0) * (1 - 2.0 ** -9) - 2.0 ** -24).all()
